@@ -13,6 +13,10 @@ Functions mirror the C entry points:
   mss_scan_status           -> scan_status(...)
   mamba2_ssd_fwd            -> ssd_fwd(...)         (include/ssd.h)
   mss_ssd_workspace_size    -> ssd_workspace_size(...)
+  gated_delta_fwd           -> gated_delta_fwd(...)       (include/gated_delta.h)
+  gated_delta_update        -> gated_delta_update(...)
+  gated_rmsnorm_fwd / _bwd  -> gated_rmsnorm_fwd / _bwd / _fn(...)  (include/norm.h)
+  add_rmsnorm_fwd / _bwd    -> add_rmsnorm_fwd / _bwd / _fn(...)
 """
 from __future__ import annotations
 
@@ -39,7 +43,11 @@ MSS_BF16 = 1
 MSS_TESTFLAG_DROP_PUBLISH = 0x1
 MSS_TESTFLAG_DEBUG_OOB = 0x2  # checked build only: one planted out-of-range y store
 
-# every symbol include/selective_scan.h and include/ssd.h declare
+MSS_DELTA_AUTO = 0
+MSS_DELTA_RECURRENT = 1
+MSS_DELTA_CHUNKED = 2
+
+# every symbol the headers in include/ declare
 EXPORTED_SYMBOLS = (
     "mss_scan_workspace_size",
     "mamba_selective_scan_fwd",
@@ -54,6 +62,15 @@ EXPORTED_SYMBOLS = (
     "mss_ssd_workspace_size",
     "mamba2_ssd_fwd",
     "mss_ssd_status",
+    "gated_delta_fwd",
+    "gated_delta_update",
+    "mss_gated_delta_status",
+    "gated_rmsnorm_fwd",
+    "gated_rmsnorm_bwd",
+    "mss_gated_rmsnorm_bwd_workspace_size",
+    "add_rmsnorm_fwd",
+    "add_rmsnorm_bwd",
+    "mss_add_rmsnorm_bwd_workspace_size",
 )
 
 
@@ -157,6 +174,74 @@ class SsdArgs(ctypes.Structure):
     ]
 
 
+class DeltaArgs(ctypes.Structure):
+    """Mirror of ``mss_delta_args``."""
+    _fields_ = [(name, ctypes.c_int64) for name in (
+        "batch", "seqlen", "nheads", "headdim", "ngroups", "dstate")] + [
+        ("in_dtype", ctypes.c_int),
+        ("out_dtype", ctypes.c_int),
+    ] + [(name, ctypes.c_void_p) for name in (
+        "q", "k", "v", "dt", "A", "beta", "dt_bias")] + [
+        ("dt_softplus", ctypes.c_int),
+        ("beta_sigmoid", ctypes.c_int),
+        ("scale", ctypes.c_float),
+    ] + [(name, ctypes.c_void_p) for name in ("h0", "y", "last_state")] + [
+        ("stride_" + name, ctypes.c_int64 * 3) for name in (
+            "q", "k", "v", "dt", "beta", "y")] + [
+        ("cu_seqlens", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int64),
+        ("plan", ctypes.c_int),
+        ("spin_timeout_ns", ctypes.c_uint64),
+    ]
+
+
+class DeltaUpdateArgs(ctypes.Structure):
+    """Mirror of ``mss_delta_update_args``."""
+    _fields_ = [(name, ctypes.c_int64) for name in (
+        "batch", "nheads", "headdim", "ngroups", "dstate")] + [
+        ("in_dtype", ctypes.c_int),
+        ("out_dtype", ctypes.c_int),
+    ] + [(name, ctypes.c_void_p) for name in (
+        "state", "q", "k", "v", "dt", "A", "beta", "dt_bias")] + [
+        ("dt_softplus", ctypes.c_int),
+        ("beta_sigmoid", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("y", ctypes.c_void_p),
+    ] + [("stride_" + name, ctypes.c_int64 * 2) for name in (
+        "q", "k", "v", "dt", "beta", "y")]
+
+
+class GatedNormArgs(ctypes.Structure):
+    """Mirror of ``mss_gated_norm_args``."""
+    _fields_ = [(name, ctypes.c_int64) for name in ("rows", "width", "group_size")] + [
+        ("dtype", ctypes.c_int),
+        ("norm_before_gate", ctypes.c_int),
+        ("shared_weight", ctypes.c_int),
+        ("eps", ctypes.c_float),
+    ] + [(name, ctypes.c_void_p) for name in (
+        "x", "z", "weight", "y", "dy", "dx", "dz", "dweight")] + [
+        ("stride_" + name, ctypes.c_int64) for name in ("x", "z", "y", "dy", "dx", "dz")] + [
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class AddNormArgs(ctypes.Structure):
+    """Mirror of ``mss_add_norm_args``."""
+    _fields_ = [(name, ctypes.c_int64) for name in ("rows", "width")] + [
+        ("dtype", ctypes.c_int),
+        ("res_dtype", ctypes.c_int),
+        ("eps", ctypes.c_float),
+    ] + [(name, ctypes.c_void_p) for name in (
+        "x", "residual", "scale", "weight", "y", "residual_out", "dy", "dresidual_out",
+        "dx", "dresidual", "dweight", "dscale")] + [
+        ("stride_" + name, ctypes.c_int64) for name in (
+            "x", "residual", "y", "residual_out", "dy", "dresidual_out", "dx", "dresidual")] + [
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 class MssError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -193,6 +278,17 @@ def _bind(lib):
     lib.mamba2_ssd_fwd.restype = ctypes.c_int
     lib.mss_ssd_status.argtypes = [ctypes.c_void_p]
     lib.mss_ssd_status.restype = ctypes.c_int
+    for name, args in (("gated_delta_fwd", DeltaArgs), ("gated_delta_update", DeltaUpdateArgs),
+                       ("gated_rmsnorm_fwd", GatedNormArgs), ("gated_rmsnorm_bwd", GatedNormArgs),
+                       ("add_rmsnorm_fwd", AddNormArgs), ("add_rmsnorm_bwd", AddNormArgs)):
+        getattr(lib, name).argtypes = [P(args), ctypes.c_void_p]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.mss_gated_delta_status.argtypes = [ctypes.c_void_p]
+    lib.mss_gated_delta_status.restype = ctypes.c_int
+    for name, args in (("mss_gated_rmsnorm_bwd_workspace_size", GatedNormArgs),
+                       ("mss_add_rmsnorm_bwd_workspace_size", AddNormArgs)):
+        getattr(lib, name).argtypes = [P(args), P(ctypes.c_size_t)]
+        getattr(lib, name).restype = ctypes.c_int
     lib.mss_abi_version.argtypes = []
     lib.mss_abi_version.restype = ctypes.c_int
     return lib
@@ -515,6 +611,10 @@ __all__ = [
     "scan_status", "make_scan_args", "load_library", "status_string",
     "MssError", "ScanArgs", "UpdateArgs", "EXPORTED_SYMBOLS", "build",
     "ssd_fwd", "make_ssd_args", "SsdArgs", "ssd_workspace_size",
+    "gated_delta_fwd", "gated_delta_update", "make_gated_delta_args", "gated_delta_status",
+    "DeltaArgs", "DeltaUpdateArgs", "gated_rmsnorm_fwd", "gated_rmsnorm_bwd",
+    "gated_rmsnorm_fn", "add_rmsnorm_fwd", "add_rmsnorm_bwd", "add_rmsnorm_fn",
+    "GatedNormArgs", "AddNormArgs",
 ]
 
 
@@ -662,3 +762,412 @@ def selective_scan_fn(u, delta, A, B, C, D=None, z=None, delta_bias=None,
     return _SelectiveScanFn.apply(_rows_view(u), _rows_view(delta), A, _rows_view(B),
                                   _rows_view(C), D, None if z is None else _rows_view(z),
                                   delta_bias, delta_softplus, h0, cu_seqlens)
+
+
+# ------------------------------------------------------- gated delta rule
+
+
+def _check_views(device, named):
+    """CUDA tensors on `device` of the given dtype and shape, each with a
+    contiguous last dimension (no shape: strides are free)."""
+    for name, t, dtype, shape, inner in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if inner == "dense" and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if inner == "rows" and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have a contiguous last dimension")
+
+
+class _on_device:
+    """The call's device as the current one while its kernels are enqueued,
+    and the stream: the caller's, or that device's current one."""
+
+    def __init__(self, device, stream):
+        self._guard = torch.cuda.device(device)
+        self._device, self._stream = device, stream
+
+    def __enter__(self):
+        self._guard.__enter__()
+        stream = self._stream
+        if stream is None:
+            stream = torch.cuda.current_stream(self._device)
+        elif stream.device != self._device:
+            self._guard.__exit__(None, None, None)
+            raise ValueError(f"stream is on {stream.device}, the tensors on {self._device}")
+        return stream
+
+    def __exit__(self, *exc):
+        self._guard.__exit__(*exc)
+
+
+def _set_strides(a, **tensors):
+    for name, (t, dims) in tensors.items():
+        dst = getattr(a, "stride_" + name)
+        for i in range(dims):
+            dst[i] = t.stride(i)
+
+
+def make_gated_delta_args(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True,
+                          beta_sigmoid=True, scale=None, h0=None, y=None, last_state=None,
+                          cu_seqlens=None, plan=MSS_DELTA_AUTO, spin_timeout_ns=0) -> DeltaArgs:
+    if not isinstance(v, torch.Tensor) or not isinstance(q, torch.Tensor):
+        raise TypeError("q and v must be CUDA tensors")
+    if v.dim() != 4 or q.dim() != 4:
+        raise ValueError("q, k and v must have the dimensions (batch, seqlen, heads, width)")
+    batch, L, H, P = v.shape
+    G, N = q.shape[2], q.shape[3]
+    ind, dev = q.dtype, q.device
+    seqs = batch
+    if cu_seqlens is not None:
+        _check_views(dev, [("cu_seqlens", cu_seqlens, torch.int32, None, "dense")])
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+        if batch != 1:
+            raise ValueError("packed sequences need batch 1")
+        seqs = cu_seqlens.numel() - 1
+    f32 = torch.float32
+    _check_views(dev, [
+        ("q", q, ind, (batch, L, G, N), "rows"), ("k", k, ind, (batch, L, G, N), "rows"),
+        ("v", v, ind, (batch, L, H, P), "rows"), ("dt", dt, ind, (batch, L, H), None),
+        ("beta", beta, ind, (batch, L, H), None), ("A", A, f32, (H,), "dense"),
+        ("dt_bias", dt_bias, f32, (H,), "dense"), ("h0", h0, f32, (seqs, H, P, N), "dense"),
+        ("last_state", last_state, f32, (seqs, H, P, N), "dense"),
+        ("y", y, None, (batch, L, H, P), "rows")])
+    a = DeltaArgs()
+    a.batch, a.seqlen, a.nheads, a.headdim, a.ngroups, a.dstate = batch, L, H, P, G, N
+    a.in_dtype = _dtype_code(ind)
+    a.out_dtype = _dtype_code(y.dtype) if y is not None else MSS_F32
+    a.q, a.k, a.v, a.dt, a.A, a.beta = (_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta))
+    a.dt_bias = _ptr(dt_bias)
+    a.dt_softplus, a.beta_sigmoid = int(bool(dt_softplus)), int(bool(beta_sigmoid))
+    a.scale = N ** -0.5 if scale is None else float(scale)
+    a.h0, a.y, a.last_state = _ptr(h0), _ptr(y), _ptr(last_state)
+    _set_strides(a, q=(q, 3), k=(k, 3), v=(v, 3), dt=(dt, 3), beta=(beta, 3))
+    if y is not None:
+        _set_strides(a, y=(y, 3))
+    if cu_seqlens is not None:
+        a.cu_seqlens, a.num_seqs = cu_seqlens.data_ptr(), seqs
+    a.plan = int(plan)
+    a.spin_timeout_ns = int(spin_timeout_ns)
+    return a
+
+
+def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_sigmoid=True,
+                    scale=None, h0=None, return_last_state=False, out_dtype=torch.float32,
+                    y=None, last_state=None, cu_seqlens=None, stream=None, check_status=False,
+                    plan=MSS_DELTA_AUTO):
+    """Gated delta rule over whole sequences through ``gated_delta_fwd``.
+
+    q, k: (batch, L, ngroups, dstate); v: (batch, L, nheads, headdim); dt,
+    beta: (batch, L, nheads), float32 or bfloat16, all the same; A, dt_bias:
+    (nheads,) float32.  q, k, v and y may be views with a contiguous last
+    dimension, dt and beta any views.  ``scale`` multiplies the readout
+    (default dstate ** -0.5).  ``cu_seqlens`` (int32 CUDA tensor of
+    num_seqs + 1 ascending offsets within 0 ... L) packs independent
+    sequences into one row (batch 1); rows of y outside them are not
+    written.  h0 and last_state: (sequences, nheads, headdim, dstate)
+    float32, and may be one tensor.  Returns y (batch, L, nheads, headdim) in
+    ``out_dtype`` (and the final states when ``return_last_state``).
+    """
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("v must have the dimensions (batch, seqlen, heads, width)")
+    if y is None:
+        y = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+    if return_last_state and last_state is None:
+        seqs = v.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+        last_state = torch.empty((seqs, v.shape[2], v.shape[3], q.shape[-1]),
+                                 dtype=torch.float32, device=v.device)
+    a = make_gated_delta_args(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale,
+                              h0, y, last_state, cu_seqlens, plan)
+    lib = load_library()
+    with _on_device(q.device, stream) as s:
+        rc = lib.gated_delta_fwd(ctypes.byref(a), _stream_handle(s))
+        if rc != MSS_OK:
+            raise MssError(rc, "gated_delta_fwd")
+        if check_status:
+            rc = lib.mss_gated_delta_status(_stream_handle(s))
+            if rc != MSS_OK:
+                raise MssError(rc, "mss_gated_delta_status")
+    return (y, last_state) if return_last_state else y
+
+
+def gated_delta_status(stream=None) -> int:
+    """Raw status code of the chunked calls completed on this device since
+    the last read (``mss_gated_delta_status``)."""
+    return load_library().mss_gated_delta_status(_stream_handle(stream))
+
+
+def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True,
+                       beta_sigmoid=True, scale=None, out_dtype=torch.float32, y=None,
+                       stream=None):
+    """One decode step through ``gated_delta_update``; ``state`` (batch,
+    nheads, headdim, dstate) float32 is updated in place.  q, k: (batch,
+    ngroups, dstate); v: (batch, nheads, headdim); dt, beta: (batch, nheads);
+    views as for ``gated_delta_fwd``.  Returns y (batch, nheads, headdim)."""
+    if not isinstance(state, torch.Tensor) or not isinstance(q, torch.Tensor):
+        raise TypeError("state and q must be CUDA tensors")
+    if state.dim() != 4 or q.dim() != 3:
+        raise ValueError("state must be (batch, heads, headdim, dstate), q (batch, groups, dstate)")
+    batch, H, P, N = state.shape
+    G, ind, dev, f32 = q.shape[1], q.dtype, q.device, torch.float32
+    if y is None:
+        y = torch.empty((batch, H, P), dtype=out_dtype, device=state.device)
+    _check_views(dev, [
+        ("state", state, f32, None, "dense"), ("q", q, ind, (batch, G, N), "rows"),
+        ("k", k, ind, (batch, G, N), "rows"), ("v", v, ind, (batch, H, P), "rows"),
+        ("dt", dt, ind, (batch, H), None), ("beta", beta, ind, (batch, H), None),
+        ("A", A, f32, (H,), "dense"), ("dt_bias", dt_bias, f32, (H,), "dense"),
+        ("y", y, None, (batch, H, P), "rows")])
+    a = DeltaUpdateArgs()
+    a.batch, a.nheads, a.headdim, a.ngroups, a.dstate = batch, H, P, G, N
+    a.in_dtype, a.out_dtype = _dtype_code(ind), _dtype_code(y.dtype)
+    a.state, a.q, a.k, a.v = _ptr(state), _ptr(q), _ptr(k), _ptr(v)
+    a.dt, a.A, a.beta, a.dt_bias, a.y = _ptr(dt), _ptr(A), _ptr(beta), _ptr(dt_bias), _ptr(y)
+    a.dt_softplus, a.beta_sigmoid = int(bool(dt_softplus)), int(bool(beta_sigmoid))
+    a.scale = N ** -0.5 if scale is None else float(scale)
+    _set_strides(a, q=(q, 2), k=(k, 2), v=(v, 2), dt=(dt, 2), beta=(beta, 2), y=(y, 2))
+    with _on_device(dev, stream) as s:
+        rc = load_library().gated_delta_update(ctypes.byref(a), _stream_handle(s))
+    if rc != MSS_OK:
+        raise MssError(rc, "gated_delta_update")
+    return y
+
+
+# ------------------------------------------- norms before and after a block
+
+
+def _rows_of(name, t):
+    """(rows, row stride) of a tensor (..., width) whose leading dimensions
+    step evenly through memory."""
+    if t.dim() < 1 or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    rows, stride = 1, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != rows * stride:
+            raise ValueError(f"the leading dimensions of {name} must be one run of rows at an "
+                             "even stride")
+        rows *= n
+    return rows, (t.shape[-1] if stride is None else stride)
+
+
+def _norm_rows(a, device, shape, named):
+    """Pointers and row strides of the (..., width) tensors of a norm call."""
+    _check_views(device, [(n, t, d, shape, "rows") for n, t, d in named])
+    for name, t, _ in named:
+        if t is not None:
+            setattr(a, name, t.data_ptr())
+            setattr(a, "stride_" + name, _rows_of(name, t)[1])
+
+
+def _norm_call(name, a, size_fn, device, stream):
+    """Runs one norm entry point, with the workspace it asks for."""
+    lib = load_library()
+    with _on_device(device, stream) as s:
+        ws = None
+        if size_fn is not None:
+            n = ctypes.c_size_t(0)
+            rc = getattr(lib, size_fn)(ctypes.byref(a), ctypes.byref(n))
+            if rc != MSS_OK:
+                raise MssError(rc, size_fn)
+            ws = alloc_workspace(int(n.value), device)
+            if ws is not None:
+                a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+        rc = getattr(lib, name)(ctypes.byref(a), _stream_handle(s))
+        if rc != MSS_OK:
+            raise MssError(rc, name)
+        if ws is not None:  # keep the workspace until the stream has used it
+            ws.record_stream(s)
+
+
+def _gated_norm_args(x, z, weight, eps, group_size, norm_before_gate):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise TypeError("x must be a CUDA tensor with at least one dimension")
+    width = x.shape[-1]
+    gs = width if group_size is None else int(group_size)
+    if gs < 1 or width % gs:
+        raise ValueError(f"group_size {gs} must divide the width {width}")
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 1 or \
+            weight.numel() not in (width, gs):
+        raise ValueError(f"weight must have {width} or {gs} entries")
+    _check_views(x.device, [("weight", weight, torch.float32, None, "dense")])
+    a = GatedNormArgs()
+    a.rows, a.width, a.group_size = _rows_of("x", x)[0], width, gs
+    a.dtype = _dtype_code(x.dtype)
+    a.norm_before_gate = int(bool(norm_before_gate))
+    a.shared_weight = int(weight.numel() == gs)
+    a.eps, a.weight = float(eps), weight.data_ptr()
+    return a
+
+
+def gated_rmsnorm_fwd(x, z, weight, eps=1e-5, group_size=None, norm_before_gate=False, y=None,
+                      stream=None):
+    """RMS norm after a block, gated by silu(z), through ``gated_rmsnorm_fwd``.
+
+    x, z: (..., width) float32 or bfloat16, rows contiguous and evenly
+    spaced; weight float32 with ``width`` entries, or ``group_size`` entries
+    shared by every group.  The norm is taken over each group of
+    ``group_size`` channels (default: the width), of x o silu(z), or of x
+    with the gate applied after it (``norm_before_gate``).  Returns y like x.
+    """
+    a = _gated_norm_args(x, z, weight, eps, group_size, norm_before_gate)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _norm_rows(a, x.device, x.shape, [("x", x, x.dtype), ("z", z, x.dtype), ("y", y, x.dtype)])
+    _norm_call("gated_rmsnorm_fwd", a, None, x.device, stream)
+    return y
+
+
+def gated_rmsnorm_bwd(x, z, weight, dy, eps=1e-5, group_size=None, norm_before_gate=False,
+                      need_dweight=True, stream=None):
+    """Gradients of sum(dy * y) for ``gated_rmsnorm_fwd`` on the same inputs.
+    Returns a dict of dx, dz (x's dtype) and dweight (float32, like weight,
+    None unless ``need_dweight``)."""
+    a = _gated_norm_args(x, z, weight, eps, group_size, norm_before_gate)
+    dx, dz = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    dw = torch.empty_like(weight) if need_dweight else None
+    _norm_rows(a, x.device, x.shape, [("x", x, x.dtype), ("z", z, x.dtype), ("dy", dy, x.dtype),
+                                      ("dx", dx, x.dtype), ("dz", dz, x.dtype)])
+    a.dweight = _ptr(dw)
+    _norm_call("gated_rmsnorm_bwd", a, "mss_gated_rmsnorm_bwd_workspace_size", x.device, stream)
+    return {"dx": dx, "dz": dz, "dweight": dw}
+
+
+def _add_norm_args(like, weight, scale, eps):
+    if not isinstance(like, torch.Tensor) or like.dim() < 1:
+        raise TypeError("x and the residual must be CUDA tensors with at least one dimension")
+    width = like.shape[-1]
+    _check_views(like.device, [("weight", weight, torch.float32, (width,), "dense"),
+                               ("scale", scale, torch.float32, (width,), "dense")])
+    a = AddNormArgs()
+    a.rows, a.width = _rows_of("x", like)[0], width
+    a.eps, a.weight, a.scale = float(eps), weight.data_ptr(), _ptr(scale)
+    return a
+
+
+def add_rmsnorm_fwd(x, residual, weight, scale=None, eps=1e-5, residual_dtype=None, y=None,
+                    residual_out=None, stream=None):
+    """Residual sum and RMS norm before a block, through ``add_rmsnorm_fwd``:
+    r = residual + scale o x and y = r / sqrt(mean(r^2) + eps) o weight.
+
+    x: (..., width) float32 or bfloat16; residual: the same shape, float32
+    or x's dtype, or None (a stream's first block; r then has
+    ``residual_dtype``, default float32); weight, scale (optional):
+    (width,) float32.  ``residual_out`` may be the residual itself.  Returns
+    (y in x's dtype, r in the residual's dtype).
+    """
+    a = _add_norm_args(x, weight, scale, eps)
+    if residual_out is None:
+        rd = residual.dtype if residual is not None else residual_dtype or torch.float32
+        residual_out = torch.empty(x.shape, dtype=rd, device=x.device)
+    rd = residual_out.dtype
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    a.dtype, a.res_dtype = _dtype_code(x.dtype), _dtype_code(rd)
+    _norm_rows(a, x.device, x.shape, [
+        ("x", x, x.dtype), ("residual", residual, rd), ("y", y, x.dtype),
+        ("residual_out", residual_out, rd)])
+    _norm_call("add_rmsnorm_fwd", a, None, x.device, stream)
+    return y, residual_out
+
+
+def add_rmsnorm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, scale=None, eps=1e-5,
+                    need_dweight=True, need_dscale=True, stream=None):
+    """Gradients for ``add_rmsnorm_fwd`` from its stored sum ``residual_out``:
+    of sum(dy * y) + sum(dresidual_out * residual_out).  x is needed for
+    dscale only.  Returns a dict of dx (dy's dtype), dresidual (the
+    residual's dtype), dweight and dscale (float32; None where not asked for
+    or there is no scale)."""
+    a = _add_norm_args(residual_out, weight, scale, eps)
+    if not isinstance(dy, torch.Tensor):
+        raise TypeError("dy must be a CUDA tensor")
+    rd, td, shape, dev = residual_out.dtype, dy.dtype, residual_out.shape, residual_out.device
+    if scale is not None and need_dscale and x is None:
+        raise ValueError("dscale needs x")
+    dx = torch.empty(shape, dtype=td, device=dev)
+    dres = torch.empty(shape, dtype=rd, device=dev)
+    dw = torch.empty_like(weight) if need_dweight else None
+    ds = torch.empty_like(scale) if scale is not None and need_dscale else None
+    a.dtype, a.res_dtype = _dtype_code(td), _dtype_code(rd)
+    _norm_rows(a, dev, shape, [
+        ("residual_out", residual_out, rd), ("dy", dy, td), ("dresidual_out", dresidual_out, rd),
+        ("x", x if ds is not None else None, td), ("dx", dx, td), ("dresidual", dres, rd)])
+    a.dweight, a.dscale = _ptr(dw), _ptr(ds)
+    _norm_call("add_rmsnorm_bwd", a, "mss_add_rmsnorm_bwd_workspace_size", dev, stream)
+    return {"dx": dx, "dresidual": dres, "dweight": dw, "dscale": ds}
+
+
+def _even_rows(t):
+    """t itself when its rows are contiguous and evenly spaced, else a copy."""
+    try:
+        _rows_of("t", t)
+        return t
+    except ValueError:
+        return t.contiguous()
+
+
+class _GatedRmsNormFn(torch.autograd.Function):
+    """Autograd wrapper of gated_rmsnorm_fwd and gated_rmsnorm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, z, weight, eps, group_size, norm_before_gate):
+        ctx.kw = dict(eps=eps, group_size=group_size, norm_before_gate=norm_before_gate)
+        ctx.save_for_backward(x, z, weight)
+        return gated_rmsnorm_fwd(x, z, weight, **ctx.kw)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, z, weight = ctx.saved_tensors
+        g = gated_rmsnorm_bwd(x, z, weight, _even_rows(dy), need_dweight=ctx.needs_input_grad[2],
+                              **ctx.kw)
+        return g["dx"], g["dz"], g["dweight"], None, None, None
+
+
+def gated_rmsnorm_fn(x, z, weight, eps=1e-5, group_size=None, norm_before_gate=False):
+    """Differentiable ``gated_rmsnorm_fwd``, with gradients for x, z and
+    weight through the CUDA backward pass."""
+    return _GatedRmsNormFn.apply(_even_rows(x), _even_rows(z), weight, eps, group_size,
+                                 norm_before_gate)
+
+
+class _AddRmsNormFn(torch.autograd.Function):
+    """Autograd wrapper of add_rmsnorm_fwd and add_rmsnorm_bwd."""
+
+    @staticmethod
+    def forward(ctx, x, residual, weight, scale, eps, residual_dtype):
+        y, res = add_rmsnorm_fwd(x, residual, weight, scale, eps, residual_dtype)
+        ctx.eps, ctx.x_dtype = eps, x.dtype
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x if scale is not None else None, weight, scale, res)
+        return y, res
+
+    @staticmethod
+    def backward(ctx, dy, dres):
+        x, weight, scale, res = ctx.saved_tensors
+        if dy is None:
+            dy = torch.zeros(res.shape, dtype=ctx.x_dtype, device=res.device)
+        g = add_rmsnorm_bwd(res, weight, _even_rows(dy),
+                            None if dres is None else _even_rows(dres), x, scale, ctx.eps,
+                            need_dweight=ctx.needs_input_grad[2],
+                            need_dscale=ctx.needs_input_grad[3])
+        return (g["dx"], g["dresidual"] if ctx.needs_input_grad[1] else None, g["dweight"],
+                g["dscale"], None, None)
+
+
+def add_rmsnorm_fn(x, residual, weight, scale=None, eps=1e-5, residual_dtype=None):
+    """Differentiable ``add_rmsnorm_fwd``: (y, residual_out), with gradients
+    for x, residual, weight and scale through the CUDA backward pass."""
+    return _AddRmsNormFn.apply(_even_rows(x), None if residual is None else _even_rows(residual),
+                               weight, scale, eps, residual_dtype)

@@ -1,0 +1,176 @@
+// norm.cuh -- shared parts of the RMS norm kernels (norm_fwd.cu,
+// norm_bwd.cu): parameters, the mapping of a row onto threads, vector loads
+// and the sums over a row.
+//
+// A row is one (token, group) pair of gs channels.  TPR threads hold it in
+// registers, NV pieces of 8 channels each, so every input is read once:
+// vectors of 8 neighbouring channels where sizes, strides and addresses
+// allow (VEC), else channels TPR apart, so that a warp's scalar accesses
+// still fall into whole sectors.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "device_math.cuh"
+#include "norm.h"
+
+namespace sss48 {
+namespace norm {
+
+constexpr int kGateAfter = 0, kGateBefore = 1, kAdd = 2;  // MODE
+constexpr int64_t kMaxGroup = 16384;
+
+struct Params {
+  int64_t rows;
+  int ng, gs;   // groups of a row, channels of a group (add: 1, width)
+  int shared;   // one weight for every group
+  float eps, inv;  // 1 / gs
+  const void *x, *z;      // add: x, residual
+  const float *weight, *scale;
+  void *y, *res;          // res: residual_out
+  const void *dy, *dres;  // dres: dresidual_out
+  void *dx, *dz;          // add: dx, dresidual
+  int64_t sx, sz, sy, sres, sdy, sdres, sdx, sdz;
+  float *part, *part2;    // partial sums of dweight, dscale
+};
+
+// Threads of a row and pieces of a thread for a group of gs channels, and
+// the threads of a block: rows of up to 512 channels fit a warp or a part of
+// one (sums by shuffles alone), longer ones take a block.
+template <int TPR_, int NV_> struct Shape {
+  static constexpr int TPR = TPR_, NV = NV_;
+  static constexpr int kThreads = TPR_ < 128 ? 128 : TPR_;
+  static constexpr int kRows = kThreads / TPR_;  // rows of a block side by side
+};
+template <typename F> auto by_shape(int64_t gs, F f) {
+  if (gs <= 64) return f(Shape<8, 1>());
+  if (gs <= 128) return f(Shape<16, 1>());
+  if (gs <= 512) return f(Shape<32, 2>());
+  if (gs <= 2048) return f(Shape<128, 2>());
+  if (gs <= 4096) return f(Shape<256, 2>());
+  if (gs <= 8192) return f(Shape<512, 2>());
+  return f(Shape<512, 4>());
+}
+
+// eight channels as they lie in memory
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = reinterpret_cast<const float4 *>(p)[0];
+    b = reinterpret_cast<const float4 *>(p)[1];
+  }
+  __device__ __forceinline__ void set(int e, float v) { reinterpret_cast<float *>(this)[e] = v; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+template <> struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    a = *reinterpret_cast<const uint4 *>(p);
+  }
+  __device__ __forceinline__ void set(int e, __nv_bfloat16 v) {
+    reinterpret_cast<__nv_bfloat16 *>(this)[e] = v;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+
+template <int TPR, bool VEC> __device__ __forceinline__ int column(int i, int e, int lane) {
+  return VEC ? (i * TPR + lane) * 8 + e : i * TPR * 8 + e * TPR + lane;
+}
+
+// piece i of a row of gs channels (zeros past its end)
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ Raw8<T> load8(const T *row, int i, int lane, int gs, bool valid) {
+  Raw8<T> r;
+  if constexpr (VEC) {
+    const int c = column<TPR, true>(i, 0, lane);
+    if (valid && c < gs) {
+      r.load(row + c);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.set(e, from_f32<T>(0.f));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = column<TPR, false>(i, e, lane);
+      r.set(e, valid && c < gs ? row[c] : from_f32<T>(0.f));
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store_vec8(float *p, const float (&v)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store_vec8(__nv_bfloat16 *p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&t);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T, int TPR, bool VEC>
+__device__ __forceinline__ void store8(T *row, int i, int lane, int gs, const float (&v)[8]) {
+  if constexpr (VEC) {
+    const int c = column<TPR, true>(i, 0, lane);
+    if (c < gs) store_vec8(row + c, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = column<TPR, false>(i, e, lane);
+      if (c < gs) row[c] = from_f32<T>(v[e]);
+    }
+  }
+}
+
+// Sums of NS values over the TPR threads of a row, given to all of them.
+// `sm` holds NS * 16 floats per call site in flight.
+template <int TPR, int NS>
+__device__ __forceinline__ void row_sum(float (&v)[NS], float *sm) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int s = 0; s < NS; ++s) v[s] += __shfl_xor_sync(0xffffffffu, v[s], o);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) sm[s * 16 + (threadIdx.x >> 5)] = v[s];
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) t += sm[s * 16 + w];
+      v[s] = t;
+    }
+  }
+}
+
+// Argument checks of a call (norm_bwd.cu): fills *p, and *vec with whether
+// every row can be moved as 16-byte vectors.
+mss_status resolve(const mss_gated_norm_args *a, bool bwd, Params *p, bool *vec);
+mss_status resolve(const mss_add_norm_args *a, bool bwd, Params *p, bool *vec);
+
+inline bool al(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline size_t esize(mss_dtype t) { return t == MSS_BF16 ? 2 : 4; }
+
+}  // namespace norm
+}  // namespace sss48
