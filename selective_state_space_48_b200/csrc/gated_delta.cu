@@ -27,6 +27,9 @@ namespace sss48 {
 namespace {
 
 constexpr int kThreads = 128;
+// steps of a sequence (packed ones: on average) from which the chunked
+// evaluation runs
+constexpr int64_t kChunkSteps = 32;
 constexpr int kGroups = kThreads / 8;  // rows of a block side by side
 
 // Four columns from `col` of a row of n columns: one vector load where VEC,
@@ -319,7 +322,18 @@ extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
   }
   p.cu = a->cu_seqlens;
   p.spin_ns = a->spin_timeout_ns ? a->spin_timeout_ns : 2000000000ull;
-  if (a->plan == MSS_DELTA_CHUNKED) return MSS_ERR_UNSUPPORTED;
+  const bool bf16 = a->in_dtype == MSS_BF16;
+  const bool applies = delta_chunk_applies(p, bf16);
+  if (a->plan == MSS_DELTA_CHUNKED && !applies) return MSS_ERR_UNSUPPORTED;
+  if (applies && (a->plan == MSS_DELTA_CHUNKED ||
+                  (a->plan == MSS_DELTA_AUTO && p.L / (packed ? seqs : 1) >= kChunkSteps))) {
+    p.status = delta_status_word();
+    if (!p.status) return MSS_ERR_CUDA;
+    return launch_delta_chunk(p, a->out_dtype == MSS_BF16, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? MSS_OK
+               : MSS_ERR_CUDA;
+  }
   return launch_delta_recurrent(p, a->in_dtype == MSS_BF16, a->out_dtype == MSS_BF16,
                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MSS_OK
@@ -382,5 +396,12 @@ extern "C" mss_status gated_delta_update(const mss_delta_update_args *a, void *s
 
 extern "C" mss_status mss_gated_delta_status(void *stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MSS_ERR_CUDA;
-  return MSS_OK;
+  unsigned *word = delta_status_word();
+  unsigned v = 0;
+  const unsigned zero = 0;
+  if (!word || cudaMemcpy(&v, word, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess)
+    return MSS_ERR_CUDA;
+  if (v && cudaMemcpy(word, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
+    return MSS_ERR_CUDA;
+  return v ? MSS_ERR_TIMEOUT : MSS_OK;
 }

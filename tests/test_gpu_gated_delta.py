@@ -61,6 +61,67 @@ def test_recurrent(size, dtype):
     check(delta_inputs(*size, dtype, h0=size[1] != 64), "recurrent")
 
 
+CHUNKED_SIZES = [(1, 64, 1, 128, 1, 128), (1, 1, 1, 128, 1, 128), (2, 63, 2, 64, 1, 64),
+                 (1, 128, 2, 128, 1, 128), (1, 129, 4, 128, 2, 128), (2, 65, 3, 8, 3, 8),
+                 (1, 200, 2, 24, 1, 40), (1, 333, 2, 136, 1, 96), (1, 70, 1, 264, 1, 72),
+                 (3, 513, 4, 128, 4, 128), (1, 1025, 2, 120, 2, 128)]
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("size", CHUNKED_SIZES)
+def test_chunked(size, out_dtype):
+    check(delta_inputs(*size, BF, seed=size[1], h0=size[1] % 2 == 1), "chunked", out_dtype)
+
+
+def test_chunked_gates():
+    """softplus and sigmoid off; strengths up to 2; hard decays (a block of
+    32 steps that loses more than 2^64) beside none at all."""
+    d = delta_inputs(1, 150, 4, 64, 2, 64, BF, h0=True, signed=True)
+    d["dt_bias"] = None
+    d["dt"] = (d["dt"].float().abs() * 0.05).to(BF)
+    d["beta"] = (2 * torch.sigmoid(d["beta"].float())).to(BF)
+    check(d, "chunked", dt_softplus=False, beta_sigmoid=False, scale=0.7)
+    d["A"] = torch.tensor([0.0, -1.0, -300.0, -40.0], device="cuda")
+    d["beta"] = (d["beta"].float() / 2).to(BF)
+    check(d, "chunked", dt_softplus=False, beta_sigmoid=False)
+
+
+def test_chunked_repeated_keys():
+    """Every key the same, full strength, no decay: A is all ones below the
+    diagonal, the state holds the last value only."""
+    d = delta_inputs(1, 200, 2, 64, 1, 64, BF)
+    d["k"] = torch.zeros_like(d["k"])
+    d["k"][..., 3] = 1
+    d["A"] = torch.zeros(2, device="cuda")
+    d["beta"] = torch.ones_like(d["beta"])
+    y, last = check(d, "chunked", beta_sigmoid=False)
+    assert worst(last[0, :, :, 3], d["v"][0, -1].double()) <= tolerance(64, 200, F32, True)
+
+
+def test_nothing_leaks_from_behind_a_sequence():
+    """Values behind a sequence's end, NaN among them, do not reach it."""
+    cu = torch.tensor([0, 70, 100], dtype=torch.int32, device="cuda")
+    d = delta_inputs(1, 140, 2, 64, 1, 64, BF)
+    want, wl = sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=True, plan=2)
+    for n in ("q", "k", "v", "dt", "beta"):
+        d[n][:, 100:] = float("nan")
+    got, gl = sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=True, plan=2)
+    assert torch.equal(got[:, :100], want[:, :100]) and torch.equal(gl, wl)
+    for n in ("q", "k", "v", "dt", "beta"):
+        d[n][:, 70:100] = float("nan")
+    got, gl = sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=True, plan=2)
+    assert torch.equal(got[:, :70], want[:, :70]) and torch.equal(gl[0], wl[0])
+
+
+def test_chunked_refusals():
+    d = delta_inputs(1, 70, 2, 64, 1, 64, F32)
+    for bad in (d, delta_inputs(1, 70, 2, 64, 1, 60, BF), delta_inputs(1, 70, 2, 60, 1, 64, BF),
+                delta_inputs(1, 70, 2, 64, 1, 136, BF)):
+        with pytest.raises(sss.MssError) as e:
+            sss.gated_delta_fwd(**bad, plan=sss.MSS_DELTA_CHUNKED)
+        assert e.value.code == sss.MSS_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("out_dtype", [F32, BF])
 def test_recurrent_output_types(out_dtype):
     check(delta_inputs(2, 50, 4, 48, 2, 40, F32), "recurrent", out_dtype)
@@ -106,7 +167,7 @@ def test_update_continues_a_prompt():
     assert worst(state, lr) <= tol
 
 
-@pytest.mark.parametrize("plan,dtype", [("recurrent", F32), ("recurrent", BF)])
+@pytest.mark.parametrize("plan,dtype", [("recurrent", F32), ("recurrent", BF), ("chunked", BF)])
 def test_packed(plan, dtype):
     """Ragged sequences with an empty and a one-token one, and rows behind
     the last: those stay as they were."""
