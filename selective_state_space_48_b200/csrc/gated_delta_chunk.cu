@@ -5,36 +5,40 @@
 // for s <= t, and H the state (headdim x dstate) before the chunk, the
 // written rows U solve
 //
-//   (I + A) U = diag(b) (V - diag(2^c) K H^T),  A[t,s] = b_t D[t,s] k_t.k_s
-//                                               for s < t.
+//   (I + A) U = diag(b) (V - diag(2^c) K H^T),
+//   A[t,s] = b_t D[t,s] k_t.k_s  for s < t,
 //
-// T = (I + A)^-1 does not depend on H, so with M = T diag(b) and
-// W = T diag(b 2^c) K only one product with H and one with U lie on the
-// chain from chunk to chunk:
+// and with T = (I + A)^-1 diag(b), which does not depend on H,
 //
-//   U^T = V^T M^T - H W^T                   M = headdim, N = t
-//   H  <- 2^(c_last) H + (U^T diag(2^(c_last - c))) K       N = dstate
-//   Y^T = H Q^T diag(2^c) + U^T (Q K^T o D)^T               N = t
+//   R^T = -(H K^T) diag(2^c)                                N = t
+//   U^T = V^T T^T + R^T T^T                                 N = t, K = s
+//   H  <- 2^(c_last) H + (U^T diag(2^(c_last - c))) K       N = dstate, K = s
+//   Y^T = (H Q^T) diag(2^c) + U^T (Q K^T o D)^T             N = t
 //
 // Everything runs transposed, headdim (128 of it per block) on the lanes of
-// tensor memory, so that H and U enter their products as the operand in
+// tensor memory, so that H, R and U enter their products as the operand in
 // tensor memory, straight from the registers of the thread that owns the row.
+// (T diag(2^c) K as an operand instead of R would take one product less on
+// the chain from chunk to chunk, but more in all, and the tensor cores were
+// the limit of that form.)
 //
-// Precision.  q, k and v are bf16 and enter exactly.  M, W, H, U and
+// Precision.  q, k and v are bf16 and enter exactly.  H, R, T, U and
 // Q K^T o D are fp32 values given as hi + lo, two bf16 values (off by 2^-18
 // at most): a product with an exact operand takes two products, one of two
 // such pairs three (lo lo is left out).  H itself stays in fp32 registers and
 // is added to there, not in the tensor cores' accumulators.
 //
-// Roles (18 warps, one block per SM: the sequence, head and 128 rows):
+// Roles (28 warps, one block per SM: the sequence, head and 128 rows):
 //   warp 0        TMA loads of the K, Q tiles (three stages) and V (two)
-//   warp 1        issues every product, in one order
-//   warps 2-9     the chain: H in registers (64 columns a thread), its pairs
-//                 and those of U into tensor memory
-//   warps 10-17   what does not depend on H, one chunk ahead: gates, A, its
-//                 inverse, M, Q K^T o D, W; and the output
-// The inverse: two 32 x 32 triangles by substitution, a column per lane, and
-// the block below them as two 32^3 products of 3 x tf32 mma.sync.
+//   warp 1        issues every product
+//   warp 2        the gates: running sums of log2 a and what follows from them
+//   warps 4-19    the chain: H in registers (32 columns a thread), its pairs
+//                 and those of R and U into tensor memory; the output, while
+//                 the next product with H runs
+//   warps 20-27   what does not depend on H, up to two chunks ahead: A, its
+//                 inverse T, Q K^T o D
+// The inverse: 16 x 16 triangles by substitution, a column per lane, then the
+// blocks below them as products, -T22 (A21 T11), in 3 x tf32 mma.sync.
 //
 // Shared memory tiles are rows of 128 bytes with the 128-byte swizzle.  Every
 // wait is bounded as in tcgen05.cuh, so no block can hang.
@@ -48,46 +52,71 @@ namespace sss48 {
 namespace {
 
 constexpr int C = 64;                 // steps of a chunk
-constexpr int kThreads = 576;
-constexpr int kGroup = 256;           // threads of the chain, and of the rest
-constexpr int kBarAux = 1;            // named barrier of warps 10-17
+constexpr int kThreads = 896;
+constexpr int kChainWarps = 16, kAuxWarps = 8;
+constexpr int kAux = kAuxWarps * 32;
+constexpr int kBarAux = 1;            // named barrier of warps 20-27
 
 constexpr int kHalf = 64 * 128;       // 64 rows of 128 bytes
 constexpr int kStageKQ = 4 * kHalf;   // K, Q of dstate 0..63, K, Q of 64..127
 constexpr int kStageV = 2 * kHalf;
 constexpr int oKQ = 0;
 constexpr int oV = 3 * kStageKQ;
-constexpr int oW = oV + 2 * kStageV;  // W^T hi, lo: [dstate][t]
-constexpr int oM = oW + 4 * kHalf;    // M hi, lo, -M diag(2^c) hi, lo: [t][s]
-constexpr int oP = oM + 4 * kHalf;    // two of (Q K^T o D) hi, lo: [t][s]
-constexpr int oArr = oP + 4 * kHalf;  // float beta, colf, cum [C]; 2 x (du, eo)
-constexpr int oBar = oArr + 7 * C * 4;
-constexpr int kBars = 21;
-constexpr int oTmemSlot = oBar + kBars * 8;
-constexpr int oAbort = oTmemSlot + 4;
-constexpr int kSmemBytes = oAbort + 4 + 1024;  // room to align the base
-static_assert(kSmemBytes <= 232448, "shared memory above the per-block limit");
-
-// the inverse's scratch lies where M is written afterwards: 32 x 32 blocks of
-// rows of 40 floats (8 rows start on 8 different groups of banks)
+constexpr int oP = oV + 2 * kStageV;  // two of (Q K^T o D) hi, lo: [t][s]
+constexpr int oT = oP + 4 * kHalf;    // two of T hi, lo: [t][s]
+constexpr int oScr = oT + 4 * kHalf;  // scratch of the inverse
+// 32 x 32 blocks, rows of 40 floats (8 rows start on 8 groups of banks)
 constexpr int kLd = 40, kBlk = 32 * kLd;
 constexpr int bA11 = 0, bA22 = 1, bA21 = 2, bT11 = 3, bT22 = 4, bZ = 5;
-static_assert(6 * kBlk * 4 <= 4 * kHalf, "scratch of the inverse");
+constexpr int oGate = oScr + 6 * kBlk * 4;  // two of (b, c) [C], 2^(c_31 - c) [32]
+constexpr int kGate = (2 * C + 32) * 4;
+constexpr int oDecay = oGate + 2 * kGate;  // three of (2^(c_last - c), 2^c, scale 2^c) [C]
+constexpr int kDecay = 3 * C * 4;
+constexpr int oBar = oDecay + 3 * kDecay;
+constexpr int kBars = 33;
+constexpr int oTmemSlot = oBar + kBars * 8;
+constexpr int oAbort = oTmemSlot + 4;
+constexpr int kSmemBytes = oAbort + 4;
+static_assert(kSmemBytes <= 232448, "shared memory above the per-block limit");
+static_assert(oGate % 16 == 0 && kGate % 16 == 0 && oDecay % 16 == 0, "16-byte vectors");
 
-// tensor memory columns
+// tensor memory columns (all 512 are allocated, so they start at 0)
 constexpr uint32_t kColH = 0;     // H pairs / the update U'^T K (128)
-constexpr uint32_t kColU = 128;   // U, then its pairs
-constexpr uint32_t kColUd = 192;  // pairs of U diag(2^(c_last - c))
-constexpr uint32_t kColO1 = 256, kColO2 = 320;
-constexpr uint32_t kColS = 384;   // K K^T (lanes 0..63), Q K^T (64..127)
-constexpr uint32_t kColW = 448;   // -W^T
+constexpr uint32_t kColX = 128;   // H K^T, then the pairs of R
+constexpr uint32_t kColU = 192;   // U, then its pairs
+constexpr uint32_t kColUd = 256;  // pairs of U' = U diag(2^(c_last - c))
+constexpr uint32_t kColO1 = 320, kColO2 = 384;
+constexpr uint32_t kColS = 448;   // K K^T (lanes 0..63), Q K^T (64..127)
 constexpr uint32_t kTmemCols = 512;
 
-// barriers: tiles landed and released; then, per chunk, products done (S, W,
-// U, O1, the update, O) and operands ready (M and P; W; H; U; O drained)
-constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 10, kDoneW = 11,
-              kDoneU = 12, kDoneO1 = 13, kDoneH = 14, kDoneO = 15, kReadyM = 16, kReadyW = 17,
-              kReadyH = 18, kReadyU = 19, kFreeO = 20;
+// Barriers.  Tiles landed and released; per chunk, products done (S, X, U,
+// O1, the update, O) and operands ready (H; R; U; T and P), S and O drained;
+// the two T and P buffers released; the gates written (the decays have three
+// buffers, the rest two) and their two and three buffers released.  A waiter may not fall two phases
+// behind: where it could, the barriers are a ring.  The groups arrive one
+// lane per warp.
+constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 10, kDoneX = 11,
+              kDoneU = 12, kDoneO1 = 13, kDoneH = 14, kDoneO = 15, kReadyH = 16, kReadyR = 17,
+              kReadyU = 18, kFreeO = 19, kFreeS = 20, kReadyT = 21, kFreeP = 23, kReadyG = 25,
+              kFreeG = 28, kFreeD = 30;  // .. 32
+// arrivals that complete a barrier's phase
+__device__ __forceinline__ int bar_count(int i) {
+  if (i == kFreeS || i == kReadyT || i == kReadyT + 1 || i == kFreeG || i == kFreeG + 1)
+    return kAuxWarps;
+  if ((i >= kReadyH && i <= kFreeO) || i >= kFreeD)
+    return kChainWarps;
+  return 1;
+}
+
+// The bounded wait of Sync, with the flag looked at only when the phase is not
+// complete yet.
+struct Waits {
+  Sync sy;
+  __device__ __forceinline__ void wait(int i, uint32_t parity) const {
+    if (!mbar_try_wait(sy.bar + i, parity)) sy.wait(i, parity);
+  }
+  __device__ __forceinline__ void drain(int i, uint32_t parity) const { sy.drain(i, parity); }
+};
 
 struct Maps {
   CUtensorMap q, k, v;
@@ -98,7 +127,72 @@ __device__ unsigned g_delta_status;
 // x = hi + lo for a pair of values, packed two to a register
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
   hi = pack_bf16(a, b);
-  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+  const float2 r = __ffma2_rn(
+      make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
+      make_float2(-1.f, -1.f), make_float2(a, b));
+  lo = pack_bf16(r.x, r.y);
+}
+__device__ __forceinline__ void split8(const float *f, uint4 &hi, uint4 &lo) {
+  split2(f[0], f[1], hi.x, lo.x);
+  split2(f[2], f[3], hi.y, lo.y);
+  split2(f[4], f[5], hi.z, lo.z);
+  split2(f[6], f[7], hi.w, lo.w);
+}
+
+// one arrival for the warp, after all its lanes' writes
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Whether phase `parity` is complete, without waiting (try_wait may suspend
+// the thread for microseconds).
+__device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok;
+}
+
+// The products are issued by one lane (`go`: elect_one's), but the whole warp
+// runs the issuing code, so that descriptors stay in uniform registers: 35
+// cycles a product of 128 x 64 x 16 with an operand in tensor memory, 52 with
+// both in shared memory; from a branch of one lane it was 50 and 52, with a
+// lane index for the predicate 65.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc, uint32_t go) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc, uint32_t go) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(go)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t go) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_addr(bar)),
+      "r"(go)
+      : "memory");
 }
 
 // c += a b, m16n8k8, tf32 operands (bits below tf32's are not read)
@@ -115,20 +209,22 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) 
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
-// One 16 x 8 tile (rows r0.., columns n0..) of X Y, 32 deep, as three tf32
-// products; X[r][k] at xa + r * xr + k * xk, Y[k][n] at yb + k * kLd + n.
-__device__ __forceinline__ void tile32(const float *xa, int xr, int xk, const float *yb, int r0,
-                                       int n0, int lane, float (&out)[4]) {
+// One 16 x 8 tile of X Y, DEPTH deep, as three tf32 products; X[r][k] at
+// xa + r * xr + k * xk, Y[k][n] at yb + k * kLd + n.  A lane gets rows
+// lane / 4 and lane / 4 + 8, columns 2 (lane % 4) and the next.
+template <int DEPTH>
+__device__ __forceinline__ void tile(const float *xa, int xr, int xk, const float *yb, int lane,
+                                     float (&out)[4]) {
   const int g = lane >> 2, t = lane & 3;
   float c0[4] = {}, c1[4] = {}, c2[4] = {};
 #pragma unroll
-  for (int k = 0; k < 32; k += 8) {
+  for (int k = 0; k < DEPTH; k += 8) {
     uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      split_tf32(xa[(r0 + g + 8 * (i & 1)) * xr + (k + t + 4 * (i >> 1)) * xk], ah[i], al[i]);
+      split_tf32(xa[(g + 8 * (i & 1)) * xr + (k + t + 4 * (i >> 1)) * xk], ah[i], al[i]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) split_tf32(yb[(k + t + 4 * i) * kLd + n0 + g], bh[i], bl[i]);
+    for (int i = 0; i < 2; ++i) split_tf32(yb[(k + t + 4 * i) * kLd + g], bh[i], bl[i]);
     mma_tf32(c0, ah, bh);
     mma_tf32(c1, al, bh);
     mma_tf32(c2, ah, bl);
@@ -136,27 +232,66 @@ __device__ __forceinline__ void tile32(const float *xa, int xr, int xk, const fl
 #pragma unroll
   for (int i = 0; i < 4; ++i) out[i] = c0[i] + (c1[i] + c2[i]);
 }
+__device__ __forceinline__ void store_tile(float *d, int lane, const float (&z)[4], float sign) {
+  d += (lane >> 2) * kLd + 2 * (lane & 3);
+  *reinterpret_cast<float2 *>(d) = make_float2(sign * z[0], sign * z[1]);
+  *reinterpret_cast<float2 *>(d + 8 * kLd) = make_float2(sign * z[2], sign * z[3]);
+}
 
-template <typename OutT>
+// T = (I + A)^-1 of a 32 x 32 block, by one warp; `a` holds A transposed.
+// Two 16 x 16 triangles at once: lane j of a half has column j, and x_s is
+// final once the steps before it have been taken out of it.  (T's block above
+// the diagonal is zero from the start.)
+__device__ __forceinline__ void invert32(const float *a, float *t, float *z, int lane) {
+  const int off = (lane >> 4) * (16 * kLd + 16), j = lane & 15;
+  float2 x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = make_float2(j == 2 * i ? 1.f : 0.f, j == 2 * i + 1 ? 1.f : 0.f);
+#pragma unroll
+  for (int s = 0; s < 16; ++s) {
+    const float xs = s & 1 ? x[s >> 1].y : x[s >> 1].x;
+    t[off + s * kLd + j] = xs;
+    const float2 m = make_float2(-xs, -xs);
+#pragma unroll
+    for (int i = (s + 1) >> 2; i < 4; ++i) {
+      // A is zero on and above the diagonal: the pair that holds row s keeps it
+      const float4 v = *reinterpret_cast<const float4 *>(a + off + s * kLd + 4 * i);
+      x[2 * i] = __ffma2_rn(make_float2(v.x, v.y), m, x[2 * i]);
+      x[2 * i + 1] = __ffma2_rn(make_float2(v.z, v.w), m, x[2 * i + 1]);
+    }
+  }
+  __syncwarp();
+  float r0[4], r1[4];
+  tile<16>(a + 16, 1, kLd, t, lane, r0);
+  tile<16>(a + 16, 1, kLd, t + 8, lane, r1);
+  store_tile(z, lane, r0, 1.f);
+  store_tile(z + 8, lane, r1, 1.f);
+  __syncwarp();
+  tile<16>(t + 16 * kLd + 16, kLd, 1, z, lane, r0);
+  tile<16>(t + 16 * kLd + 16, kLd, 1, z + 8, lane, r1);
+  store_tile(t + 16 * kLd, lane, r0, -1.f);
+  store_tile(t + 16 * kLd + 8, lane, r1, -1.f);
+}
+
+// NK: 16-wide slices of dstate (4 up to 64, else 8; TMA pads with zeros).
+template <typename OutT, int NK>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *sm = reinterpret_cast<unsigned char *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // the swizzle needs 1024-byte tiles; a block without static shared memory
+  // has its dynamic memory on such a boundary
+  extern __shared__ __align__(1024) unsigned char sm[];
   const uint32_t sbase = smem_addr(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler
 
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + oBar);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + oTmemSlot);
   volatile int *abort = reinterpret_cast<volatile int *>(sm + oAbort);
-  float *beta_s = reinterpret_cast<float *>(sm + oArr);
-  float *colf_s = beta_s + C, *cum_s = colf_s + C;
-  float *dueo_s = cum_s + C;  // [2][du, eo][C]
-  const Sync sy{bar, abort, p.status, p.spin_ns};
+  const Waits sy{{bar, abort, p.status, p.spin_ns}};
 
   if (tid == 0) {
-    for (int i = 0; i < kReadyM; ++i) mbar_init(bar + i, 1);
-    for (int i = kReadyM; i < kBars; ++i) mbar_init(bar + i, kGroup);
+    for (int i = 0; i < kBars; ++i) mbar_init(bar + i, bar_count(i));
     *abort = 0;
     fence_mbar_init();
   }
@@ -164,7 +299,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // (an allocation of every column starts at 0; the addresses below rely on it)
+  if (*tmem_slot != 0) {
+    *abort = 1;
+    if (tid == 0) atomicOr(p.status, static_cast<unsigned>(MSS_ERR_TIMEOUT));
+  }
 
   const int slices = static_cast<int>((p.P + 127) / 128);
   const int64_t sh = blockIdx.x / slices;
@@ -176,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t b64, t0, t1;
   delta_span(p, s, b64, t0, t1);
   const int b = static_cast<int>(b64);
-  const int nc = static_cast<int>((t1 - t0 + C - 1) / C);
+  const int nc = __shfl_sync(0xffffffffu, static_cast<int>((t1 - t0 + C - 1) / C), 0);
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
@@ -204,235 +343,133 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------- tensor-core issue
-    if (lane == 0 && nc > 0) {
-      constexpr uint32_t idKK = idesc_bf16(128, 64, 0, 0);   // both K-major
-      constexpr uint32_t idTK = idesc_bf16(128, 64, 1, 0);   // A as stored by step
-      constexpr uint32_t idKT = idesc_bf16(128, 64, 0, 1);   // B as stored by step
-      const uint32_t idH = idesc_bf16(128, N <= 64 ? 64 : 128, 0, 1);
-      const int nk = (N + 15) >> 4;  // 16-wide slices of dstate
-      const uint64_t dW = smem_desc(sbase + oW, 16, 1024);
-      const uint64_t dM = smem_desc(sbase + oM, 16, 1024);
-      constexpr uint64_t kLo = 2 * kHalf >> 4;  // hi -> lo of W; M to M diag(2^c)
-      constexpr uint64_t kLoM = kHalf >> 4;     // hi -> lo of M and P
-      auto stage = [&](int i) { return sbase + oKQ + (i % 3) * kStageKQ; };
-      // slice k of a K-major tile in 64-wide halves `half` bytes apart
-      auto kslice = [](int k, uint64_t half) {
-        return static_cast<uint64_t>(k >> 2) * (half >> 4) + (k & 3) * 2;
-      };
-      auto scores = [&](int i) {  // [K; Q] K^T
-        sy.wait(kFullKQ + i % 3, (i / 3) & 1);
-        tc_fence_after();
-        if (!*abort) {
-          const uint64_t d = smem_desc(stage(i), 16, 1024);
-          for (int k = 0; k < nk; ++k) {
-            const uint64_t o = kslice(k, 2 * kHalf);
-            umma_bf16(tmem + kColS, d + o, d + o, idKK, k > 0);
-          }
-        }
-        umma_commit(bar + kDoneS);
-      };
-      // -W^T = K^T (-M diag(2^c))^T and U^T = V^T M^T of chunk i
-      auto ahead = [&](int i) {
-        sy.wait(kReadyM, i & 1);
-        tc_fence_after();
-        if (!*abort) {
-          const uint64_t dK = smem_desc(stage(i), 2 * kHalf, 1024);
+    constexpr uint32_t idKK = idesc_bf16(128, 64, 0, 0);       // both K-major
+    constexpr uint32_t idTK = idesc_bf16(128, 64, 1, 0);       // A as stored by step
+    constexpr uint32_t idH = idesc_bf16(128, 16 * NK, 0, 1);  // B as stored by step
+    constexpr uint64_t kLo = kHalf >> 4;  // hi -> lo of T and P
+    const uint32_t on = elect_one();
+    // slice k of a K-major tile whose 64-wide halves lie 2 kHalf apart
+    auto kslice = [](int k) { return static_cast<uint64_t>((k >> 2) * (2 * kHalf >> 4) + (k & 3) * 2); };
+    // after a timeout nothing is issued any more (commits still complete)
+    auto alive = [&]() { return !__any_sync(0xffffffffu, *abort); };
+    auto ready = [&](int i, uint32_t parity) {
+      return __shfl_sync(0xffffffffu, mbar_test(bar + i, parity), 0) != 0;
+    };
+    int ns = 0, sst = 0;  // the next chunk whose S = [K; Q] K^T is due, ns % 3
+    auto issue_scores = [&]() {
+      tc_fence_after();
+      if (alive()) {
+        const uint64_t d = smem_desc(sbase + oKQ + sst * kStageKQ, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16(tmem + kColW, dK + (k & 3) * 128, dM + kLo + (k >> 2) * kLoM + (k & 3) * 2,
-                      idTK, k > 0);
-        }
-        umma_commit(bar + kDoneW);
-        if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of chunk i - 1 has been read
-        sy.wait(kFullV + (i & 1), (i / 2) & 1);
-        tc_fence_after();
-        if (!*abort) {
-          const uint64_t dV = smem_desc(sbase + oV + (i & 1) * kStageV, kHalf, 1024);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_bf16(tmem + kColU, dV + (k & 3) * 128, dM + (k >> 2) * kLoM + (k & 3) * 2, idTK,
-                      k > 0);
-        }
-        umma_commit(bar + kEmptyV + (i & 1));
-      };
-      scores(0);
-      ahead(0);
-      if (nc > 1) scores(1);
-      for (int i = 0; i < nc; ++i) {
-        const uint32_t st = stage(i);
-        sy.wait(kReadyW, i & 1);
-        sy.wait(kReadyH, i & 1);
-        tc_fence_after();
-        if (!*abort) {  // U^T -= H W^T
-          for (int k = 0; k < nk; ++k) {
-            const uint32_t hi = tmem + kColH + (k >> 2) * 64 + (k & 3) * 8;
-            umma_bf16_ts(tmem + kColU, hi, dW + k * 128, idKT, 1);
-            umma_bf16_ts(tmem + kColU, hi + 32, dW + k * 128, idKT, 1);
-            umma_bf16_ts(tmem + kColU, hi, dW + kLo + k * 128, idKT, 1);
-          }
-        }
-        umma_commit(bar + kDoneU);
-        if (i > 0) {
-          sy.wait(kFreeO, (i - 1) & 1);
-          tc_fence_after();
-        }
-        if (!*abort) {  // O1 = H Q^T
-          const uint64_t dQ = smem_desc(st + kHalf, 16, 1024);
-          for (int k = 0; k < nk; ++k) {
-            const uint32_t hi = tmem + kColH + (k >> 2) * 64 + (k & 3) * 8;
-            const uint64_t o = dQ + kslice(k, 2 * kHalf);
-            umma_bf16_ts(tmem + kColO1, hi, o, idKK, k > 0);
-            umma_bf16_ts(tmem + kColO1, hi + 32, o, idKK, 1);
-          }
-        }
-        umma_commit(bar + kDoneO1);
-        sy.wait(kReadyU, i & 1);
-        sy.wait(kDoneO1, i & 1);  // the update overwrites the pairs of H
-        tc_fence_after();
-        if (!*abort) {  // U'^T K
-          const uint64_t dK = smem_desc(st, 2 * kHalf, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t hi = tmem + kColUd + (k >> 1) * 32 + (k & 1) * 8;
-            umma_bf16_ts(tmem + kColH, hi, dK + k * 128, idH, k > 0);
-            umma_bf16_ts(tmem + kColH, hi + 16, dK + k * 128, idH, 1);
-          }
-        }
-        umma_commit(bar + kDoneH);
-        umma_commit(bar + kEmptyKQ + i % 3);
-        if (!*abort) {  // O2 = U^T (Q K^T o D)^T
-          const uint64_t dP = smem_desc(sbase + oP + (i & 1) * 2 * kHalf, 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t hi = tmem + kColU + (k >> 1) * 32 + (k & 1) * 8;
-            umma_bf16_ts(tmem + kColO2, hi, dP + k * 2, idKK, k > 0);
-            umma_bf16_ts(tmem + kColO2, hi + 16, dP + k * 2, idKK, 1);
-            umma_bf16_ts(tmem + kColO2, hi, dP + kLoM + k * 2, idKK, 1);
-          }
-        }
-        umma_commit(bar + kDoneO);
-        if (i + 1 < nc) ahead(i + 1);
-        if (i + 2 < nc) scores(i + 2);
+        for (int k = 0; k < NK; ++k) mma_ss(kColS, d + kslice(k), d + kslice(k), idKK, k > 0, on);
       }
-      // every product done before the tensor memory is freed
-      sy.drain(kDoneO, (nc - 1) & 1);
-    }
-    __syncwarp();
-  } else if (warp < 10) {
-    // -------------------------------------------------------- the chain
-    const int q = warp & 3, e = (warp - 2) >> 2;
-    const int row = p0 + 32 * q + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const int64_t base = (sh * p.P + row) * p.N + 64 * e;
-    float H[64];
-#pragma unroll
-    for (int j = 0; j < 64; j += 4) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.h0 && row < P && 64 * e + j < N)
-        v = __ldcs(reinterpret_cast<const float4 *>(p.h0 + base + j));
-      H[j] = v.x;
-      H[j + 1] = v.y;
-      H[j + 2] = v.z;
-      H[j + 3] = v.w;
-    }
-    float gam = 1.0f;
+      mma_commit(bar + kDoneS, on);
+      ++ns;
+      sst = sst == 2 ? 0 : sst + 1;
+    };
+    // S as early as its tiles and its place allow, without waiting
+    auto try_scores = [&]() {
+      if (ns < nc && (ns == 0 || ready(kFreeS, (ns - 1) & 1)) && ready(kFullKQ + sst, (ns / 3) & 1))
+        issue_scores();
+    };
+    int st = 0;  // i % 3
     for (int i = 0; i < nc; ++i) {
+      const uint32_t kq = sbase + oKQ + st * kStageKQ;
+      while (ns <= i) {
+        if (ns > 0) sy.wait(kFreeS, (ns - 1) & 1);
+        sy.wait(kFullKQ + sst, (ns / 3) & 1);
+        issue_scores();
+      }
+      sy.wait(kReadyH, i & 1);
+      tc_fence_after();
+      if (alive()) {  // X = H K^T
+        const uint64_t dK = smem_desc(kq, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
+          mma_ts(kColX, hi, dK + kslice(k), idKK, k > 0, on);
+          mma_ts(kColX, hi + 16, dK + kslice(k), idKK, 1, on);
+        }
+      }
+      mma_commit(bar + kDoneX, on);
+      try_scores();
+      const uint64_t dT = smem_desc(sbase + oT + (i & 1) * 2 * kHalf, 16, 1024);
+      sy.wait(kReadyT + (i & 1), (i / 2) & 1);
+      sy.wait(kFullV + (i & 1), (i / 2) & 1);
+      if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of the chunk before has been read
+      tc_fence_after();
+      if (alive()) {  // U^T = V^T T^T
+        const uint64_t dV = smem_desc(sbase + oV + (i & 1) * kStageV, kHalf, 1024);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mma_ss(kColU, dV + k * 128, dT + k * 2, idTK, k > 0, on);
+          mma_ss(kColU, dV + k * 128, dT + kLo + k * 2, idTK, 1, on);
+        }
+      }
+      mma_commit(bar + kEmptyV + (i & 1), on);
+      sy.wait(kReadyR, i & 1);
+      tc_fence_after();
+      if (alive()) {  // U^T += R^T T^T
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          mma_ts(kColU, kColX + 16 * k, dT + k * 2, idKK, 1, on);
+          mma_ts(kColU, kColX + 16 * k + 8, dT + k * 2, idKK, 1, on);
+          mma_ts(kColU, kColX + 16 * k, dT + kLo + k * 2, idKK, 1, on);
+        }
+      }
+      mma_commit(bar + kDoneU, on);
+      try_scores();
       if (i > 0) {
-        sy.wait(kDoneH, (i - 1) & 1);
+        sy.wait(kFreeO, (i - 1) & 1);
         tc_fence_after();
+      }
+      if (alive()) {  // O1 = H Q^T
+        const uint64_t dQ = smem_desc(kq + kHalf, 16, 1024);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[16];
-          tmem_ld16(tl + kColH + 64 * e + 16 * c, v);
-          tmem_wait_ld(v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            H[16 * c + j] = fmaf(gam, H[16 * c + j], __uint_as_float(v[j]));
+        for (int k = 0; k < NK; ++k) {
+          const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
+          mma_ts(kColO1, hi, dQ + kslice(k), idKK, k > 0, on);
+          mma_ts(kColO1, hi + 16, dQ + kslice(k), idKK, 1, on);
         }
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) split2(H[16 * c + 2 * j], H[16 * c + 2 * j + 1], hi[j], lo[j]);
-        tmem_st8(tl + kColH + 64 * e + 8 * c, hi);
-        tmem_st8(tl + kColH + 64 * e + 32 + 8 * c, lo);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar + kReadyH);
-
-      sy.wait(kReadyW, i & 1);  // (the gates' arrays, too)
-      const float *du = dueo_s + (i & 1) * 2 * C, *eo = du + C;
-      gam = eo[C - 1];
-      sy.wait(kDoneU, i & 1);
+      mma_commit(bar + kDoneO1, on);
+      try_scores();
+      sy.wait(kReadyU, i & 1);
+      sy.wait(kDoneO1, i & 1);  // the update overwrites the pairs of H
       tc_fence_after();
-      {
-        // 32 steps of a thread, their pairs in the columns they came from
-        uint32_t v[2][16];
-        tmem_ld16(tl + kColU + 32 * e, v[0]);
-        tmem_ld16(tl + kColU + 32 * e + 16, v[1]);
-        tmem_wait_ld(v[0]);
-        tmem_wait_ld(v[1]);
+      if (alive()) {  // U'^T K
+        const uint64_t dK = smem_desc(kq, 2 * kHalf, 1024);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            split2(__uint_as_float(v[c][2 * j]) * du[32 * e + 16 * c + 2 * j],
-                   __uint_as_float(v[c][2 * j + 1]) * du[32 * e + 16 * c + 2 * j + 1], hi[j],
-                   lo[j]);
-          tmem_st8(tl + kColUd + 32 * e + 8 * c, hi);
-          tmem_st8(tl + kColUd + 32 * e + 16 + 8 * c, lo);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            split2(__uint_as_float(v[c][2 * j]), __uint_as_float(v[c][2 * j + 1]), hi[j], lo[j]);
-          tmem_st8(tl + kColU + 32 * e + 8 * c, hi);
-          tmem_st8(tl + kColU + 32 * e + 16 + 8 * c, lo);
+        for (int k = 0; k < 4; ++k) {
+          mma_ts(kColH, kColUd + 16 * k, dK + k * 128, idH, k > 0, on);
+          mma_ts(kColH, kColUd + 16 * k + 8, dK + k * 128, idH, 1, on);
         }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar + kReadyU);
-    }
-    if (nc > 0) {
-      sy.wait(kDoneH, (nc - 1) & 1);
-      tc_fence_after();
+      mma_commit(bar + kDoneH, on);
+      mma_commit(bar + kEmptyKQ + st, on);
+      if (alive()) {  // O2 = U^T (Q K^T o D)^T
+        const uint64_t dP = smem_desc(sbase + oP + (i & 1) * 2 * kHalf, 16, 1024);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[16];
-        tmem_ld16(tl + kColH + 64 * e + 16 * c, v);
-        tmem_wait_ld(v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          H[16 * c + j] = fmaf(gam, H[16 * c + j], __uint_as_float(v[j]));
+        for (int k = 0; k < 4; ++k) {
+          mma_ts(kColO2, kColU + 16 * k, dP + k * 2, idKK, k > 0, on);
+          mma_ts(kColO2, kColU + 16 * k + 8, dP + k * 2, idKK, 1, on);
+          mma_ts(kColO2, kColU + 16 * k, dP + kLo + k * 2, idKK, 1, on);
+        }
       }
+      mma_commit(bar + kDoneO, on);
+      mma_commit(bar + kFreeP + (i & 1), on);
+      try_scores();
+      st = st == 2 ? 0 : st + 1;
     }
-    if (p.last && row < P) {
-#pragma unroll
-      for (int j = 0; j < 64; j += 4)
-        if (64 * e + j < N)
-          __stcs(reinterpret_cast<float4 *>(p.last + base + j),
-                 make_float4(H[j], H[j + 1], H[j + 2], H[j + 3]));
-    }
-  } else {
-    // --------------------------------- what does not depend on H; output
-    const int q = warp & 3, e = (warp - 10) >> 2, at = tid - 320, aw = at >> 5;
-    const uint32_t tl = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    float *scr = reinterpret_cast<float *>(sm + oM);
+    // every product done before the tensor memory is freed
+    if (nc > 0) sy.drain(kDoneO, (nc - 1) & 1);
+  } else if (warp == 2) {
+    // --------------------------------------------------------- the gates
     const __nv_bfloat16 *dtp = static_cast<const __nv_bfloat16 *>(p.dt) + b * p.sdt[0] + h * p.sdt[2];
     const __nv_bfloat16 *bp =
         static_cast<const __nv_bfloat16 *>(p.beta) + b * p.sbeta[0] + h * p.sbeta[2];
     const float A2 = p.A[h] * kLog2e, bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-    OutT *yp = static_cast<OutT *>(p.y) + b * p.sy[0] + h * p.sy[2] + t0 * p.sy[1];
-    const int row = p0 + 32 * q + lane;
-
-    // the blocks of P above the diagonal stay zero
-    for (int k = at; k < 2 * 2 * 32 * 4; k += kGroup)
-      *reinterpret_cast<uint4 *>(sm + oP + (k >> 7) * kHalf + swz((k >> 2) & 31, 4 + (k & 3))) =
-          make_uint4(0u, 0u, 0u, 0u);
-
-    // raw gates of two steps of a lane (warp 0 of the group), a chunk ahead
+    // raw values of two steps of a lane, a chunk ahead
     unsigned short rd[2] = {0, 0}, rb[2] = {0, 0};
     auto raw = [&](int j) {
 #pragma unroll
@@ -444,254 +481,357 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    if (aw == 0 && nc > 0) raw(0);
-
-    // y rows of chunk i: scale (2^c O1 + O2)
+    if (nc > 0) raw(0);
+    for (int i = 0; i < nc; ++i) {
+      const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C;
+      float g2[2], bt[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        g2[k] = bt[k] = 0.f;
+        if (32 * k + lane < left)
+          delta_gates<__nv_bfloat16>(p, __uint_as_float(static_cast<uint32_t>(rd[k]) << 16),
+                                     __uint_as_float(static_cast<uint32_t>(rb[k]) << 16), A2, bias,
+                                     g2[k], bt[k]);
+      }
+      raw(i + 1);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float x0 = __shfl_up_sync(0xffffffffu, g2[0], o);
+        const float x1 = __shfl_up_sync(0xffffffffu, g2[1], o);
+        if (lane >= o) {
+          g2[0] += x0;
+          g2[1] += x1;
+        }
+      }
+      const float end0 = __shfl_sync(0xffffffffu, g2[0], 31);
+      g2[1] += end0;
+      const float end1 = __shfl_sync(0xffffffffu, g2[1], 31);
+      if (i >= 2) sy.wait(kFreeG + (i & 1), (i / 2 - 1) & 1);
+      if (i >= 3) sy.wait(kFreeD + i % 3, (i / 3 - 1) & 1);
+      float *beta_s = reinterpret_cast<float *>(sm + oGate + (i & 1) * kGate), *cum_s = beta_s + C;
+      float *du = reinterpret_cast<float *>(sm + oDecay + (i % 3) * kDecay);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int t = 32 * k + lane;
+        const float eo = ex2_mufu(g2[k]);
+        cum_s[t] = g2[k];
+        beta_s[t] = bt[k];
+        du[t] = ex2_mufu(end1 - g2[k]);
+        du[C + t] = eo;
+        du[2 * C + t] = p.scale * eo;
+      }
+      cum_s[C + lane] = ex2_mufu(end0 - g2[0]);
+      warp_arrive(bar + kReadyG + i % 3, lane);
+    }
+  } else if (warp >= 4 && warp < 20) {
+    // -------------------------------------------------------- the chain
+    const int q = warp & 3, e = (warp - 4) >> 2;
+    const int row = p0 + 32 * q + lane;
+    const uint32_t tl = static_cast<uint32_t>(32 * q) << 16;
+    const int64_t base = (sh * p.P + row) * p.N + 32 * e;
+    OutT *yp = static_cast<OutT *>(p.y) + b * p.sy[0] + h * p.sy[2] + (t0 + 16 * e) * p.sy[1] + row;
+    float H[32];
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (p.h0 && row < P && 32 * e + j < N)
+        v = __ldcs(reinterpret_cast<const float4 *>(p.h0 + base + j));
+      H[j] = v.x;
+      H[j + 1] = v.y;
+      H[j + 2] = v.z;
+      H[j + 3] = v.w;
+    }
+    float gam = 1.0f;
+    // H <- 2^(c_last) H + U'^T K of chunk i
+    auto update = [&](int i) {
+      sy.wait(kDoneH, i & 1);
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[16];
+        tmem_ld16(tl + kColH + 32 * e + 16 * c, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float2 n = __ffma2_rn(make_float2(gam, gam),
+                                      make_float2(H[16 * c + j], H[16 * c + j + 1]),
+                                      make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+          H[16 * c + j] = n.x;
+          H[16 * c + j + 1] = n.y;
+        }
+      }
+    };
+    // y rows of chunk i, 16 steps of a thread: scale 2^c O1 + O2 (P holds the
+    // scale of O2)
     auto output = [&](int i) {
       sy.wait(kDoneO, i & 1);
       tc_fence_after();
-      const float *eo = dueo_s + (i & 1) * 2 * C + C;
-      const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C;
-      OutT *yr = yp + (static_cast<int64_t>(i) * C + 32 * e) * p.sy[1] + row;
-      float o[32];
+      const float *eo = reinterpret_cast<const float *>(sm + oDecay + (i % 3) * kDecay) + 2 * C + 16 * e;
+      uint32_t v[16], w[16];
+      tmem_ld16(tl + kColO1 + 16 * e, v);
+      tmem_ld16(tl + kColO2 + 16 * e, w);
+      tmem_wait_ld(v);
+      tmem_wait_ld(w);
+      float o[16];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[16], w[16];
-        tmem_ld16(tl + kColO1 + 32 * e + 16 * c, v);
-        tmem_ld16(tl + kColO2 + 32 * e + 16 * c, w);
-        tmem_wait_ld(v);
-        tmem_wait_ld(w);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          o[16 * c + j] = p.scale * fmaf(eo[32 * e + 16 * c + j], __uint_as_float(v[j]),
-                                         __uint_as_float(w[j]));
-      }
+      for (int j = 0; j < 16; ++j)
+        o[j] = fmaf(eo[j], __uint_as_float(v[j]), __uint_as_float(w[j]));
       tc_fence_before();
-      mbar_arrive(bar + kFreeO);
+      warp_arrive(bar + kFreeO, lane);
+      if (lane == 0) mbar_arrive(bar + kFreeD + i % 3);
+      const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C - 16 * e;
+      OutT *yr = yp + static_cast<int64_t>(i) * C * p.sy[1];
       if (row < P) {
+        if (left >= 16) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (32 * e + j < left) yr[j * p.sy[1]] = from_f32<OutT>(o[j]);
+          for (int j = 0; j < 16; ++j) yr[j * p.sy[1]] = from_f32<OutT>(o[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j < left) yr[j * p.sy[1]] = from_f32<OutT>(o[j]);
+        }
       }
     };
-
     for (int i = 0; i < nc; ++i) {
+      if (i > 0) update(i - 1);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) split2(H[16 * c + 2 * j], H[16 * c + 2 * j + 1], hi[j], lo[j]);
+        tmem_st8(tl + kColH + 32 * e + 8 * c, hi);
+        tmem_st8(tl + kColH + 32 * e + 16 + 8 * c, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar + kReadyH, lane);
+      if (i > 0) output(i - 1);
+
+      const float *du = reinterpret_cast<const float *>(sm + oDecay + (i % 3) * kDecay);
+      sy.wait(kReadyG + i % 3, (i / 3) & 1);
+      sy.wait(kDoneX, i & 1);
+      tc_fence_after();
+      {
+        // R = -2^c x, 16 steps of a thread, its pairs in the columns that x
+        // came from; nothing of the steps behind the sequence
+        uint32_t x[16], hi[8], lo[8];
+        tmem_ld16(tl + kColX + 16 * e, x);
+        const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C - 16 * e;
+        const float *ec = du + C + 16 * e;
+        tmem_wait_ld(x);
+        if (left < 16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (j >= left) x[j] = 0u;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 w = *reinterpret_cast<const float4 *>(ec + j);
+          split2(-w.x * __uint_as_float(x[j]), -w.y * __uint_as_float(x[j + 1]), hi[j / 2],
+                 lo[j / 2]);
+          split2(-w.z * __uint_as_float(x[j + 2]), -w.w * __uint_as_float(x[j + 3]),
+                 hi[j / 2 + 1], lo[j / 2 + 1]);
+        }
+        tmem_st8(tl + kColX + 16 * e, hi);
+        tmem_st8(tl + kColX + 16 * e + 8, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar + kReadyR, lane);
+
+      sy.wait(kDoneU, i & 1);
+      gam = du[2 * C - 1];
+      tc_fence_after();
+      {
+        uint32_t v[16], hi[8], lo[8];
+        tmem_ld16(tl + kColU + 16 * e, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 d = *reinterpret_cast<const float4 *>(du + 16 * e + j);
+          split2(__uint_as_float(v[j]) * d.x, __uint_as_float(v[j + 1]) * d.y, hi[j / 2], lo[j / 2]);
+          split2(__uint_as_float(v[j + 2]) * d.z, __uint_as_float(v[j + 3]) * d.w, hi[j / 2 + 1],
+                 lo[j / 2 + 1]);
+        }
+        tmem_st8(tl + kColUd + 16 * e, hi);
+        tmem_st8(tl + kColUd + 16 * e + 8, lo);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          split2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), hi[j], lo[j]);
+        tmem_st8(tl + kColU + 16 * e, hi);
+        tmem_st8(tl + kColU + 16 * e + 8, lo);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      warp_arrive(bar + kReadyU, lane);
+    }
+    if (nc > 0) {
+      update(nc - 1);
+      output(nc - 1);
+    }
+    if (p.last && row < P) {
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        if (32 * e + j < N)
+          __stcs(reinterpret_cast<float4 *>(p.last + base + j),
+                 make_float4(H[j], H[j + 1], H[j + 2], H[j + 3]));
+    }
+  } else if (warp >= 20) {
+    // ------------------------------------- what does not depend on H
+    const int q = warp & 3, e = (warp - 20) >> 2, at = tid - 640, aw = warp - 20;
+    const uint32_t tl = static_cast<uint32_t>(32 * q) << 16;
+    float *scr = reinterpret_cast<float *>(sm + oScr);
+
+    // the blocks of P and T above the diagonal stay zero, and so does that of
+    // the two 32 x 32 inverses
+    for (int k = at; k < 8 * 32 * 4; k += kAux)
+      *reinterpret_cast<uint4 *>(sm + oP + (k >> 7) * kHalf + swz((k >> 2) & 31, 4 + (k & 3))) =
+          make_uint4(0u, 0u, 0u, 0u);
+    for (int k = at; k < 2 * 16 * 16; k += kAux)
+      scr[(k < 256 ? bT11 : bT22) * kBlk + ((k >> 4) & 15) * kLd + 16 + (k & 15)] = 0.f;
+    bar_sync(kBarAux, kAux);
+
+    int st = 0;  // i % 3
+    for (int i = 0; i < nc; ++i, st = st == 2 ? 0 : st + 1) {
       const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C;
       const int len = left < C ? static_cast<int>(left) : C;
-      float *du = dueo_s + (i & 1) * 2 * C, *eo = du + C;
-      if (aw == 0) {
-        // these arrays' last readers: the output of chunk i - 2
-        if (i > 1) sy.wait(kFreeO, i & 1);
-        float g2[2], bt[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          g2[k] = bt[k] = 0.f;
-          if (32 * k + lane < len)
-            delta_gates<__nv_bfloat16>(p, __uint_as_float(static_cast<uint32_t>(rd[k]) << 16),
-                                       __uint_as_float(static_cast<uint32_t>(rb[k]) << 16), A2,
-                                       bias, g2[k], bt[k]);
-        }
-        raw(i + 1);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float x0 = __shfl_up_sync(0xffffffffu, g2[0], o);
-          const float x1 = __shfl_up_sync(0xffffffffu, g2[1], o);
-          if (lane >= o) {
-            g2[0] += x0;
-            g2[1] += x1;
-          }
-        }
-        const float end0 = __shfl_sync(0xffffffffu, g2[0], 31);
-        g2[1] += end0;
-        const float end1 = __shfl_sync(0xffffffffu, g2[1], 31);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int t = 32 * k + lane;
-          cum_s[t] = g2[k];
-          beta_s[t] = bt[k];
-          colf_s[t] = ex2_mufu((k ? end1 : end0) - g2[k]);
-          du[t] = ex2_mufu(end1 - g2[k]);
-          eo[t] = ex2_mufu(g2[k]);
-        }
-      }
-      // M of the chunk before has been read: its place is free
-      if (i > 0) sy.wait(kEmptyV + ((i - 1) & 1), ((i - 1) >> 1) & 1);
+      const float *beta_s = reinterpret_cast<const float *>(sm + oGate + (i & 1) * kGate);
+      const float *cum_s = beta_s + C, *colf_s = cum_s + C;
+      const float *du = reinterpret_cast<const float *>(sm + oDecay + st * kDecay);
+      unsigned char *tt = sm + oT + (i & 1) * 2 * kHalf;
+      sy.wait(kReadyG + st, (i / 3) & 1);
       sy.wait(kDoneS, i & 1);
+      if (i >= 2) {  // the buffers that U and O2 of chunk i - 2 read
+        sy.wait(kFreeP + (i & 1), (i / 2 - 1) & 1);
+      }
       tc_fence_after();
-      bar_sync(kBarAux, kGroup);
 
       if (len < C) {
-        // steps of whatever lies behind the sequence: nothing of them may
-        // enter a product (zero times a NaN would)
-        sy.wait(kFullKQ + i % 3, (i / 3) & 1);
+        // keys and values of whatever lies behind the sequence: nothing of
+        // them may enter a product over steps (zero times a NaN would)
+        sy.wait(kFullKQ + st, (i / 3) & 1);
         sy.wait(kFullV + (i & 1), (i / 2) & 1);
         const int rows = C - len;
-        for (int k = at; k < rows * 32; k += kGroup) {
+        for (int k = at; k < rows * 32; k += kAux) {
           const int r = len + (k >> 5), c = k & 31;
-          unsigned char *d = c < 16 ? sm + oKQ + (i % 3) * kStageKQ + (c >> 3) * 2 * kHalf
+          unsigned char *d = c < 16 ? sm + oKQ + st * kStageKQ + (c >> 3) * 2 * kHalf
                                     : sm + oV + (i & 1) * kStageV + ((c >> 3) & 1) * kHalf;
           *reinterpret_cast<uint4 *>(d + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
 
-      // rows of A (lanes 0..63 of S) and of Q K^T o D (64..127), 32 columns
-      // of a thread: below the diagonal 2^(c_t - c_end) colf[s], c_end the
-      // end of s's block of 32, both at most 1; in a diagonal block the same
-      // two factors unless the first could overflow, else one 2^x each
-      if (e <= (q & 1)) {
-        const int blk = q & 1, t = 32 * blk + lane;
-        const bool diag = e == blk, isA = q < 2;
-        uint32_t v[32];
-        tmem_ld32(tl + kColS + 32 * e, v);
+      // rows of A (lanes 0..63 of S) and of scale Q K^T o D (64..127), 32 columns
+      // of a thread: below the diagonal 2^(c_t - c_end) 2^(c_end - c_s),
+      // c_end the end of s's block of 32, both at most 1; in a diagonal block
+      // the same two factors unless the first could overflow, else one 2^x
+      // each
+      const int blk = q & 1;
+      const bool diag = e == blk, isA = q < 2;
+      if (e <= blk) {
+        const int t = 32 * blk + lane;
         const float cend = cum_s[32 * e + 31], ct = cum_s[t];
-        const float rowf = isA ? beta_s[t] : 1.0f;
+        const float rowf = isA ? beta_s[t] : p.scale;
         const bool fact = !diag || cum_s[32 * e] - cend < 64.0f;
         const float rf = rowf * ex2_mufu(ct - cend);
-        const int last = diag ? (isA ? lane : lane + 1) : 32;  // columns kept
-        tmem_wait_ld(v);
-        float f[32];
-        if (fact) {
+        const float *cf = e ? du + 32 : colf_s;
+        // columns kept
+        const int last = t >= len ? 0 : (diag ? (isA ? lane : lane + 1) : 32);
+        unsigned char *d = sm + oP + (i & 1) * 2 * kHalf;
+        float *da = scr + (diag ? (blk ? bA22 : bA11) : bA21) * kBlk + lane;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            f[j] = j < last && t < len ? __uint_as_float(v[j]) * (rf * colf_s[32 * e + j]) : 0.f;
-        } else {
+        for (int c = 0; c < 2; ++c) {
+          uint32_t v[16];
+          float f[16];
+          tmem_ld16(tl + kColS + 32 * e + 16 * c, v);
+          if (fact) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            f[j] = j < last && t < len
-                       ? __uint_as_float(v[j]) * (rowf * ex2_mufu(ct - cum_s[32 * e + j]))
-                       : 0.f;
-        }
-        if (isA) {  // transposed: the substitution reads columns of A
-          float *d = scr + (diag ? (blk ? bA22 : bA11) : bA21) * kBlk + lane;
+            for (int j = 0; j < 16; j += 4) {
+              const float4 x = *reinterpret_cast<const float4 *>(cf + 16 * c + j);
+              f[j] = rf * x.x;
+              f[j + 1] = rf * x.y;
+              f[j + 2] = rf * x.z;
+              f[j + 3] = rf * x.w;
+            }
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) d[j * kLd] = f[j];
-        } else {
-          unsigned char *d = sm + oP + (i & 1) * 2 * kHalf;
+            for (int j = 0; j < 16; ++j) f[j] = rowf * ex2_mufu(ct - cum_s[32 * e + 16 * c + j]);
+          }
+          tmem_wait_ld(v);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t hi[4], lo[4];
+          for (int j = 0; j < 16; ++j)
+            f[j] = 16 * c + j < last ? f[j] * __uint_as_float(v[j]) : 0.f;
+          if (isA) {  // transposed: the substitution reads columns of A
 #pragma unroll
-            for (int k = 0; k < 4; ++k) split2(f[8 * c + 2 * k], f[8 * c + 2 * k + 1], hi[k], lo[k]);
-            const uint32_t o = swz(t, 4 * e + c);
-            *reinterpret_cast<uint4 *>(d + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(d + kHalf + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int j = 0; j < 16; ++j) da[(16 * c + j) * kLd] = f[j];
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint4 hi, lo;
+              split8(f + 8 * k, hi, lo);
+              const uint32_t o = swz(t, 4 * e + 2 * c + k);
+              *reinterpret_cast<uint4 *>(d + o) = hi;
+              *reinterpret_cast<uint4 *>(d + kHalf + o) = lo;
+            }
           }
         }
       }
       tc_fence_before();
-      bar_sync(kBarAux, kGroup);
-
-      if (aw < 2) {
-        // column `lane` of T11 / T22: x_s is final once the steps before it
-        // have been taken out of it
-        const float *a = scr + (aw ? bA22 : bA11) * kBlk;
-        float *d = scr + (aw ? bT22 : bT11) * kBlk + lane;
-        float2 x[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          x[j] = make_float2(lane == 2 * j ? 1.f : 0.f, lane == 2 * j + 1 ? 1.f : 0.f);
-#pragma unroll
-        for (int t = 0; t < 32; ++t) {
-          const float xt = t & 1 ? x[t >> 1].y : x[t >> 1].x;
-          d[t * kLd] = xt;
-          const float2 m = make_float2(-xt, -xt);
-#pragma unroll
-          for (int j = (t + 1) >> 2; j < 8; ++j) {
-            // A is zero on and above the diagonal, so the pair that holds
-            // row t itself keeps it
-            const float4 av = *reinterpret_cast<const float4 *>(a + t * kLd + 4 * j);
-            x[2 * j] = __ffma2_rn(make_float2(av.x, av.y), m, x[2 * j]);
-            x[2 * j + 1] = __ffma2_rn(make_float2(av.z, av.w), m, x[2 * j + 1]);
-          }
-        }
-      }
-      bar_sync(kBarAux, kGroup);
+      warp_arrive(bar + kFreeS, lane);
+      // the warps of the two diagonal blocks of A invert them
+      if (isA && diag)
+        invert32(scr + (blk ? bA22 : bA11) * kBlk, scr + (blk ? bT22 : bT11) * kBlk,
+                 scr + bZ * kBlk + blk * 16 * kLd, lane);
+      bar_sync(kBarAux, kAux);
       // T21 = -T22 (A21 T11)
-      const int r0 = 16 * (aw >> 2), n0 = 8 * (aw & 3), fr = r0 + (lane >> 2),
-                fc = n0 + 2 * (lane & 3);
+      const int r0 = 16 * (aw >> 2), n0 = 8 * (aw & 3);
       float z[4];
-      tile32(scr + bA21 * kBlk, 1, kLd, scr + bT11 * kBlk, r0, n0, lane, z);
-      *reinterpret_cast<float2 *>(scr + bZ * kBlk + fr * kLd + fc) = make_float2(z[0], z[1]);
-      *reinterpret_cast<float2 *>(scr + bZ * kBlk + (fr + 8) * kLd + fc) = make_float2(z[2], z[3]);
-      bar_sync(kBarAux, kGroup);
-      tile32(scr + bT22 * kBlk, kLd, 1, scr + bZ * kBlk, r0, n0, lane, z);
-      float *t21 = scr + bA21 * kBlk;
-      *reinterpret_cast<float2 *>(t21 + fr * kLd + fc) = make_float2(-z[0], -z[1]);
-      *reinterpret_cast<float2 *>(t21 + (fr + 8) * kLd + fc) = make_float2(-z[2], -z[3]);
-      bar_sync(kBarAux, kGroup);
+      tile<32>(scr + bA21 * kBlk + r0, 1, kLd, scr + bT11 * kBlk + n0, lane, z);
+      store_tile(scr + bZ * kBlk + r0 * kLd + n0, lane, z, 1.f);
       {
-        // M = T diag(b) and -M diag(2^c): row t, columns 16c .. 16c + 15
-        const int t = at >> 2, c = at & 3;
-        float f[16];
-        const bool upper = t < 32 && c >= 2;
-        const float *src = scr + (t < 32 ? bT11 : (c < 2 ? bA21 : bT22)) * kBlk + (t & 31) * kLd +
-                           16 * (c & 1);
+        // pairs of T11 and T22, times b: 8 columns of a row
+        const int w = at >> 7, r = (at >> 2) & 31, c = at & 3;
+        const float *src = scr + (w ? bT22 : bT11) * kBlk + r * kLd + 8 * c;
+        float f[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 v = *reinterpret_cast<const float4 *>(src + 4 * j);
-          f[4 * j] = v.x;
-          f[4 * j + 1] = v.y;
-          f[4 * j + 2] = v.z;
-          f[4 * j + 3] = v.w;
+        for (int j = 0; j < 8; j += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(src + j);
+          const float4 x = *reinterpret_cast<const float4 *>(beta_s + 32 * w + 8 * c + j);
+          f[j] = v.x * x.x;
+          f[j + 1] = v.y * x.y;
+          f[j + 2] = v.z * x.z;
+          f[j + 3] = v.w * x.w;
         }
-        bar_sync(kBarAux, kGroup);  // the scratch has been read
+        uint4 hi, lo;
+        split8(f, hi, lo);
+        const uint32_t o = swz(32 * w + r, 4 * w + c);
+        *reinterpret_cast<uint4 *>(tt + o) = hi;
+        *reinterpret_cast<uint4 *>(tt + kHalf + o) = lo;
+      }
+      bar_sync(kBarAux, kAux);
+      const float2 nb = *reinterpret_cast<const float2 *>(beta_s + n0 + 2 * (lane & 3));
+      tile<32>(scr + bT22 * kBlk + r0 * kLd, kLd, 1, scr + bZ * kBlk + n0, lane, z);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = upper ? 0.f : f[j] * beta_s[16 * c + j];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          unsigned char *d = sm + oM + w * 2 * kHalf;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              split2(f[8 * k + 2 * j], f[8 * k + 2 * j + 1], hi[j], lo[j]);
-            const uint32_t o = swz(t, 2 * c + k);
-            *reinterpret_cast<uint4 *>(d + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(d + kHalf + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) f[j] *= -eo[16 * c + j];
-        }
+      for (int k = 0; k < 2; ++k) {
+        uint32_t hi, lo;
+        split2(-z[2 * k] * nb.x, -z[2 * k + 1] * nb.y, hi, lo);
+        const uint32_t o = swz(32 + r0 + 8 * k + (lane >> 2), aw & 3) + 4 * (lane & 3);
+        *reinterpret_cast<uint32_t *>(tt + o) = hi;
+        *reinterpret_cast<uint32_t *>(tt + kHalf + o) = lo;
       }
       fence_async_smem();
-      mbar_arrive(bar + kReadyM);
-
-      // -W^T rows n = 32 q + lane, steps 32 e .. 32 e + 31
-      if (i > 0) sy.wait(kDoneU, (i - 1) & 1);  // W of the chunk before has been read
-      sy.wait(kDoneW, i & 1);
-      tc_fence_after();
-      {
-        uint32_t v[32];
-        tmem_ld32(tl + kColW + 32 * e, v);
-        tmem_wait_ld(v);
-        unsigned char *d = sm + oW;
-        const int n = 32 * q + lane;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            split2(__uint_as_float(v[8 * c + 2 * k]), __uint_as_float(v[8 * c + 2 * k + 1]), hi[k],
-                   lo[k]);
-          const uint32_t o = swz(n, 4 * e + c);
-          *reinterpret_cast<uint4 *>(d + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(d + 2 * kHalf + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_async_smem();
-      tc_fence_before();
-      mbar_arrive(bar + kReadyW);
-      if (i > 0) output(i - 1);
+      warp_arrive(bar + kReadyT + (i & 1), lane);
+      if (lane == 0) mbar_arrive(bar + kFreeG + (i & 1));
+      // (the next chunk's A overwrites what the last product read: the
+      // barrier after its inverses comes too late for that)
+      bar_sync(kBarAux, kAux);
     }
-    if (nc > 0) output(nc - 1);
   }
 
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(*tmem_slot, kTmemCols);
   }
 }
 
@@ -757,7 +897,9 @@ cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t
     kernel<<<grid, kThreads, kSmemBytes, stream>>>(maps, p);
     return cudaGetLastError();
   };
-  return out_bf16 ? run(delta_chunk_kernel<__nv_bfloat16>) : run(delta_chunk_kernel<float>);
+  if (p.N <= 64)
+    return out_bf16 ? run(delta_chunk_kernel<__nv_bfloat16, 4>) : run(delta_chunk_kernel<float, 4>);
+  return out_bf16 ? run(delta_chunk_kernel<__nv_bfloat16, 8>) : run(delta_chunk_kernel<float, 8>);
 }
 
 }  // namespace sss48
