@@ -29,14 +29,15 @@
 // is added to there, not in the tensor cores' accumulators.
 //
 // Roles (28 warps, one block per SM: the sequence, head and 128 rows):
-//   warp 0        TMA loads of the K, Q tiles (three stages) and V (two)
+//   warps 0, 3    TMA loads of the K, Q tiles (three stages); of V (one)
 //   warp 1        issues every product
 //   warp 2        the gates: running sums of log2 a and what follows from them
 //   warps 4-19    the chain: H in registers (32 columns a thread), its pairs
 //                 and those of R and U into tensor memory; the output, while
 //                 the next product with H runs
-//   warps 20-27   what does not depend on H, up to two chunks ahead: A, its
-//                 inverse T, Q K^T o D
+//   warps 20-27   what does not depend on H: A, its inverse T, Q K^T o D; two
+//                 groups of four that take chunks in turn, since a chunk takes
+//                 them longer than the chain takes for one
 // The inverse: 16 x 16 triangles by substitution, a column per lane, then the
 // blocks below them as products, -T22 (A21 T11), in 3 x tf32 mma.sync.
 //
@@ -53,23 +54,25 @@ namespace {
 
 constexpr int C = 64;                 // steps of a chunk
 constexpr int kThreads = 896;
-constexpr int kChainWarps = 16, kAuxWarps = 8;
+constexpr int kChainWarps = 16, kAuxWarps = 4;  // kAuxWarps of each group
 constexpr int kAux = kAuxWarps * 32;
-constexpr int kBarAux = 1;            // named barrier of warps 20-27
+// named barriers of a group (+ its number): all of it; the A22 block handed on
+constexpr int kBarAux = 1, kBarA22 = 3;
 
 constexpr int kHalf = 64 * 128;       // 64 rows of 128 bytes
 constexpr int kStageKQ = 4 * kHalf;   // K, Q of dstate 0..63, K, Q of 64..127
 constexpr int kStageV = 2 * kHalf;
 constexpr int oKQ = 0;
 constexpr int oV = 3 * kStageKQ;
-constexpr int oP = oV + 2 * kStageV;  // two of (Q K^T o D) hi, lo: [t][s]
+constexpr int oP = oV + kStageV;      // two of (Q K^T o D) hi, lo: [t][s]
 constexpr int oT = oP + 4 * kHalf;    // two of T hi, lo: [t][s]
-constexpr int oScr = oT + 4 * kHalf;  // scratch of the inverse
-// 32 x 32 blocks, rows of 40 floats (8 rows start on 8 groups of banks)
+constexpr int oScr = oT + 4 * kHalf;  // scratch of the inverse, for each group
+// 32 x 32 blocks, rows of 40 floats (8 rows start on 8 groups of banks): A,
+// transposed, then T in the diagonal ones; A21 T11
 constexpr int kLd = 40, kBlk = 32 * kLd;
-constexpr int bA11 = 0, bA22 = 1, bA21 = 2, bT11 = 3, bT22 = 4, bZ = 5;
-constexpr int oGate = oScr + 6 * kBlk * 4;  // two of (b, c) [C], 2^(c_31 - c) [32]
-constexpr int kGate = (2 * C + 32) * 4;
+constexpr int bA11 = 0, bA22 = 1, bA21 = 2, bZ = 3;
+constexpr int oGate = oScr + 2 * 4 * kBlk * 4;  // two of (b, c) [C]
+constexpr int kGate = 2 * C * 4;
 constexpr int oDecay = oGate + 2 * kGate;  // three of (2^(c_last - c), 2^c, scale 2^c) [C]
 constexpr int kDecay = 3 * C * 4;
 constexpr int oBar = oDecay + 3 * kDecay;
@@ -95,7 +98,7 @@ constexpr uint32_t kTmemCols = 512;
 // buffers, the rest two) and their two and three buffers released.  A waiter may not fall two phases
 // behind: where it could, the barriers are a ring.  The groups arrive one
 // lane per warp.
-constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 10, kDoneX = 11,
+constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 9, kDoneX = 11,
               kDoneU = 12, kDoneO1 = 13, kDoneH = 14, kDoneO = 15, kReadyH = 16, kReadyR = 17,
               kReadyU = 18, kFreeO = 19, kFreeS = 20, kReadyT = 21, kFreeP = 23, kReadyG = 25,
               kFreeG = 28, kFreeD = 30;  // .. 32
@@ -108,18 +111,61 @@ __device__ __forceinline__ int bar_count(int i) {
   return 1;
 }
 
-// The bounded wait of Sync, with the flag looked at only when the phase is not
-// complete yet.
+// Bounded waits, short since every one is inlined: instructions from beyond
+// the instruction caches were what bounded a longer form of this kernel.  A
+// wait gives up after `limit` tries, each of which suspends the thread for up
+// to kTryNs; then, and once any wait of the block has given up, every wait
+// that is not complete returns (the results are garbage, but nothing hangs),
+// and the block's end records the timeout.
+constexpr uint32_t kTryNs = 20000;
 struct Waits {
-  Sync sy;
-  __device__ __forceinline__ void wait(int i, uint32_t parity) const {
-    if (!mbar_try_wait(sy.bar + i, parity)) sy.wait(i, parity);
+  uint32_t bar;  // shared-memory address of the barriers
+  volatile int *abort;
+  uint32_t limit;
+  __device__ __forceinline__ bool try_wait(int i, uint32_t parity) const {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar + 8 * i), "r"(parity), "r"(kTryNs)
+        : "memory");
+    return ok != 0;
   }
-  __device__ __forceinline__ void drain(int i, uint32_t parity) const { sy.drain(i, parity); }
+  // Whether the phase is complete, without waiting.
+  __device__ __forceinline__ bool test(int i, uint32_t parity) const {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar + 8 * i), "r"(parity)
+        : "memory");
+    return ok != 0;
+  }
+  // (every lane tries: about 110 cycles for a phase that is complete, 250 and
+  // more for one lane and a __syncwarp)
+  __device__ __forceinline__ void wait(int i, uint32_t parity) const {
+    uint32_t n = 0;
+    while (!try_wait(i, parity)) {
+      if (*abort) break;
+      if (++n >= limit) *abort = 1;
+    }
+  }
+  // not cut short by another wait's timeout: for copies and products still in
+  // flight at the end
+  __device__ __forceinline__ void drain(int i, uint32_t parity) const {
+    uint32_t n = 0;
+    while (!try_wait(i, parity))
+      if (++n >= limit) {
+        *abort = 1;
+        break;
+      }
+  }
 };
 
 struct Maps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, y;
 };
 
 __device__ unsigned g_delta_status;
@@ -139,23 +185,32 @@ __device__ __forceinline__ void split8(const float *f, uint4 &hi, uint4 &lo) {
   split2(f[6], f[7], hi.w, lo.w);
 }
 
+// 16 columns of this thread's lane (and 16 more from `b`), waited for: with
+// the wait in the same statement the registers are free to be any
+__device__ __forceinline__ void tmem_get16(uint32_t a, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_get16x2(uint32_t a, uint32_t b, float (&v)[16],
+                                             float (&w)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7]), "=f"(w[8]), "=f"(w[9]), "=f"(w[10]), "=f"(w[11]), "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15])
+      : "r"(a), "r"(b)
+      : "memory");
+}
+
 // one arrival for the warp, after all its lanes' writes
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-}
-
-// Whether phase `parity` is complete, without waiting (try_wait may suspend
-// the thread for microseconds).
-__device__ __forceinline__ uint32_t mbar_test(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok;
 }
 
 // The products are issued by one lane (`go`: elect_one's), but the whole warp
@@ -170,20 +225,29 @@ __device__ __forceinline__ uint32_t elect_one() {
       : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+// A descriptor is given as its low word (address, leading offset); the high
+// word is the same for all: rows of 8 groups 1024 bytes apart, version 1,
+// 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFF) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t acc, uint32_t go) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(go)
+      "{\n .reg .pred p, q;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.ne.b32 q, %5, 0;\n mov.b64 da, {%1, %6};\n mov.b64 db, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(go), "n"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        uint32_t acc, uint32_t go) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(go)
+      "{\n .reg .pred p, q;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+      " setp.ne.b32 q, %5, 0;\n mov.b64 db, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(go), "n"(kDescHi)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t go) {
@@ -209,40 +273,51 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) 
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
-// One 16 x 8 tile of X Y, DEPTH deep, as three tf32 products; X[r][k] at
-// xa + r * xr + k * xk, Y[k][n] at yb + k * kLd + n.  A lane gets rows
-// lane / 4 and lane / 4 + 8, columns 2 (lane % 4) and the next.
+// Two neighbouring 16 x 8 tiles of X Y, DEPTH deep, as three tf32 products
+// each; X[r][k] at xa + r * xr + k * xk, Y[k][n] at yb + k * kLd + n.  A lane
+// gets rows lane / 4 and lane / 4 + 8, columns 2 (lane % 4) and the next of
+// either tile.
 template <int DEPTH>
-__device__ __forceinline__ void tile(const float *xa, int xr, int xk, const float *yb, int lane,
-                                     float (&out)[4]) {
+__device__ __forceinline__ void tiles(const float *xa, int xr, int xk, const float *yb, int lane,
+                                      float (&out)[2][4]) {
   const int g = lane >> 2, t = lane & 3;
-  float c0[4] = {}, c1[4] = {}, c2[4] = {};
-#pragma unroll
+  float c0[2][4] = {}, c1[2][4] = {}, c2[2][4] = {};
+#pragma unroll 2
   for (int k = 0; k < DEPTH; k += 8) {
     uint32_t ah[4], al[4], bh[2], bl[2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       split_tf32(xa[(g + 8 * (i & 1)) * xr + (k + t + 4 * (i >> 1)) * xk], ah[i], al[i]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) split_tf32(yb[(k + t + 4 * i) * kLd + g], bh[i], bl[i]);
-    mma_tf32(c0, ah, bh);
-    mma_tf32(c1, al, bh);
-    mma_tf32(c2, ah, bl);
+    for (int n = 0; n < 2; ++n) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) split_tf32(yb[(k + t + 4 * i) * kLd + 8 * n + g], bh[i], bl[i]);
+      mma_tf32(c0[n], ah, bh);
+      mma_tf32(c1[n], al, bh);
+      mma_tf32(c2[n], ah, bl);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) out[i] = c0[i] + (c1[i] + c2[i]);
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[n][i] = c0[n][i] + (c1[n][i] + c2[n][i]);
 }
-__device__ __forceinline__ void store_tile(float *d, int lane, const float (&z)[4], float sign) {
+__device__ __forceinline__ void store_tiles(float *d, int lane, const float (&z)[2][4],
+                                            float sign) {
   d += (lane >> 2) * kLd + 2 * (lane & 3);
-  *reinterpret_cast<float2 *>(d) = make_float2(sign * z[0], sign * z[1]);
-  *reinterpret_cast<float2 *>(d + 8 * kLd) = make_float2(sign * z[2], sign * z[3]);
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    *reinterpret_cast<float2 *>(d + 8 * n) = make_float2(sign * z[n][0], sign * z[n][1]);
+    *reinterpret_cast<float2 *>(d + 8 * kLd + 8 * n) = make_float2(sign * z[n][2], sign * z[n][3]);
+  }
 }
 
-// T = (I + A)^-1 of a 32 x 32 block, by one warp; `a` holds A transposed.
-// Two 16 x 16 triangles at once: lane j of a half has column j, and x_s is
-// final once the steps before it have been taken out of it.  (T's block above
-// the diagonal is zero from the start.)
-__device__ __forceinline__ void invert32(const float *a, float *t, float *z, int lane) {
+// (I + A)^-1 of a 32 x 32 block in place, by one warp; `a` holds A transposed
+// on entry.  Two 16 x 16 triangles at once: lane j of a half has column j, and
+// x_s is final once the steps before it have been taken out of it; then
+// T21 = -T22 (A21 T11), with A21 in the upper right 16 x 16 of `a`, and its
+// products in the lower left.
+__device__ __forceinline__ void invert32(float *a, int lane) {
   const int off = (lane >> 4) * (16 * kLd + 16), j = lane & 15;
   float2 x[8];
 #pragma unroll
@@ -251,33 +326,41 @@ __device__ __forceinline__ void invert32(const float *a, float *t, float *z, int
 #pragma unroll
   for (int s = 0; s < 16; ++s) {
     const float xs = s & 1 ? x[s >> 1].y : x[s >> 1].x;
-    t[off + s * kLd + j] = xs;
     const float2 m = make_float2(-xs, -xs);
+    float4 v[4];
+#pragma unroll
+    for (int i = (s + 1) >> 2; i < 4; ++i)
+      v[i] = *reinterpret_cast<const float4 *>(a + off + s * kLd + 4 * i);
+    __syncwarp();  // the row has been read: x_s takes its place
+    a[off + s * kLd + j] = xs;
 #pragma unroll
     for (int i = (s + 1) >> 2; i < 4; ++i) {
       // A is zero on and above the diagonal: the pair that holds row s keeps it
-      const float4 v = *reinterpret_cast<const float4 *>(a + off + s * kLd + 4 * i);
-      x[2 * i] = __ffma2_rn(make_float2(v.x, v.y), m, x[2 * i]);
-      x[2 * i + 1] = __ffma2_rn(make_float2(v.z, v.w), m, x[2 * i + 1]);
+      x[2 * i] = __ffma2_rn(make_float2(v[i].x, v[i].y), m, x[2 * i]);
+      x[2 * i + 1] = __ffma2_rn(make_float2(v[i].z, v[i].w), m, x[2 * i + 1]);
     }
   }
   __syncwarp();
-  float r0[4], r1[4];
-  tile<16>(a + 16, 1, kLd, t, lane, r0);
-  tile<16>(a + 16, 1, kLd, t + 8, lane, r1);
-  store_tile(z, lane, r0, 1.f);
-  store_tile(z + 8, lane, r1, 1.f);
+  float z[2][4];
+  tiles<16>(a + 16, 1, kLd, a, lane, z);
+  store_tiles(a + 16 * kLd, lane, z, 1.f);
   __syncwarp();
-  tile<16>(t + 16 * kLd + 16, kLd, 1, z, lane, r0);
-  tile<16>(t + 16 * kLd + 16, kLd, 1, z + 8, lane, r1);
-  store_tile(t + 16 * kLd, lane, r0, -1.f);
-  store_tile(t + 16 * kLd + 8, lane, r1, -1.f);
+  tiles<16>(a + 16 * kLd + 16, kLd, 1, a + 16 * kLd, lane, z);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)  // above the diagonal T is zero
+    *reinterpret_cast<float4 *>(a + (lane >> 1) * kLd + 16 + 8 * (lane & 1) + 4 * i) =
+        make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncwarp();
+  store_tiles(a + 16 * kLd, lane, z, -1.f);
 }
 
 // NK: 16-wide slices of dstate (4 up to 64, else 8; TMA pads with zeros).
+// y_tma: whole chunks of y go out through the Q tile of their stage and a TMA
+// store (bf16 rows that a tensor map takes): 16 two-byte stores of a thread
+// straight to memory took 1.3 us of a chunk's 4.5.
 template <typename OutT, int NK>
 __global__ void __launch_bounds__(kThreads, 1)
-    delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p) {
+    delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p, const int y_tma) {
   // the swizzle needs 1024-byte tiles; a block without static shared memory
   // has its dynamic memory on such a boundary
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -288,7 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + oBar);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + oTmemSlot);
   volatile int *abort = reinterpret_cast<volatile int *>(sm + oAbort);
-  const Waits sy{{bar, abort, p.status, p.spin_ns}};
+  const uint64_t tries = p.spin_ns / kTryNs + 1;
+  const Waits sy{smem_addr(bar), abort,
+                 tries < 0xffffffffull ? static_cast<uint32_t>(tries) : 0xffffffffu};
 
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i) mbar_init(bar + i, bar_count(i));
@@ -300,10 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   // (an allocation of every column starts at 0; the addresses below rely on it)
-  if (*tmem_slot != 0) {
-    *abort = 1;
-    if (tid == 0) atomicOr(p.status, static_cast<unsigned>(MSS_ERR_TIMEOUT));
-  }
+  if (*tmem_slot != 0) *abort = 1;
 
   const int slices = static_cast<int>((p.P + 127) / 128);
   const int64_t sh = blockIdx.x / slices;
@@ -315,14 +397,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   int64_t b64, t0, t1;
   delta_span(p, s, b64, t0, t1);
   const int b = static_cast<int>(b64);
-  const int nc = __shfl_sync(0xffffffffu, static_cast<int>((t1 - t0 + C - 1) / C), 0);
+  const int total = static_cast<int>(t1 - t0);
+  const int nc = __shfl_sync(0xffffffffu, (total + C - 1) / C, 0);
 
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     if (lane == 0) {
       for (int i = 0; i < nc; ++i) {
         const int t = static_cast<int>(t0) + i * C;
-        const int a = i % 3, v = i & 1;
+        const int a = i % 3;
         if (i >= 3) sy.wait(kEmptyKQ + a, (i / 3 - 1) & 1);
         unsigned char *d = sm + oKQ + a * kStageKQ;
         mbar_expect_tx(bar + kFullKQ + a, kStageKQ);
@@ -330,14 +413,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d(d + kHalf, &maps.q, 0, g, t, b, bar + kFullKQ + a);
         tma_load_4d(d + 2 * kHalf, &maps.k, 64, g, t, b, bar + kFullKQ + a);
         tma_load_4d(d + 3 * kHalf, &maps.q, 64, g, t, b, bar + kFullKQ + a);
-        if (i >= 2) sy.wait(kEmptyV + v, (i / 2 - 1) & 1);
-        d = sm + oV + v * kStageV;
-        mbar_expect_tx(bar + kFullV + v, kStageV);
-        tma_load_4d(d, &maps.v, p0, h, t, b, bar + kFullV + v);
-        tma_load_4d(d + kHalf, &maps.v, p0 + 64, h, t, b, bar + kFullV + v);
       }
       // no copy may still be landing when the block exits
       for (int i = nc > 3 ? nc - 3 : 0; i < nc; ++i) sy.drain(kFullKQ + i % 3, (i / 3) & 1);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // (a producer of its own: V waits for its one place, K and Q run ahead)
+    if (lane == 0) {
+      for (int i = 0; i < nc; ++i) {
+        if (i >= 1) sy.wait(kEmptyV, (i - 1) & 1);
+        const int t = static_cast<int>(t0) + i * C;
+        uint64_t *full = bar + kFullV + (i & 1);
+        mbar_expect_tx(full, kStageV);
+        tma_load_4d(sm + oV, &maps.v, p0, h, t, b, full);
+        tma_load_4d(sm + oV + kHalf, &maps.v, p0 + 64, h, t, b, full);
+      }
       for (int i = nc > 2 ? nc - 2 : 0; i < nc; ++i) sy.drain(kFullV + (i & 1), (i / 2) & 1);
     }
     __syncwarp();
@@ -346,24 +437,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idKK = idesc_bf16(128, 64, 0, 0);       // both K-major
     constexpr uint32_t idTK = idesc_bf16(128, 64, 1, 0);       // A as stored by step
     constexpr uint32_t idH = idesc_bf16(128, 16 * NK, 0, 1);  // B as stored by step
-    constexpr uint64_t kLo = kHalf >> 4;  // hi -> lo of T and P
+    constexpr uint32_t kLo = kHalf >> 4;  // hi -> lo of T and P
     const uint32_t on = elect_one();
     // slice k of a K-major tile whose 64-wide halves lie 2 kHalf apart
-    auto kslice = [](int k) { return static_cast<uint64_t>((k >> 2) * (2 * kHalf >> 4) + (k & 3) * 2); };
+    auto kslice = [](int k) { return static_cast<uint32_t>((k >> 2) * (2 * kHalf >> 4) + (k & 3) * 2); };
     // after a timeout nothing is issued any more (commits still complete)
     auto alive = [&]() { return !__any_sync(0xffffffffu, *abort); };
     auto ready = [&](int i, uint32_t parity) {
-      return __shfl_sync(0xffffffffu, mbar_test(bar + i, parity), 0) != 0;
+      return __shfl_sync(0xffffffffu, sy.test(i, parity), 0) != 0;
     };
     int ns = 0, sst = 0;  // the next chunk whose S = [K; Q] K^T is due, ns % 3
     auto issue_scores = [&]() {
       tc_fence_after();
       if (alive()) {
-        const uint64_t d = smem_desc(sbase + oKQ + sst * kStageKQ, 16, 1024);
-#pragma unroll
+        const uint32_t d = desc_lo(sbase + oKQ + sst * kStageKQ, 16);
+#pragma unroll 4
         for (int k = 0; k < NK; ++k) mma_ss(kColS, d + kslice(k), d + kslice(k), idKK, k > 0, on);
       }
-      mma_commit(bar + kDoneS, on);
+      mma_commit(bar + kDoneS + (ns & 1), on);
       ++ns;
       sst = sst == 2 ? 0 : sst + 1;
     };
@@ -371,6 +462,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto try_scores = [&]() {
       if (ns < nc && (ns == 0 || ready(kFreeS, (ns - 1) & 1)) && ready(kFullKQ + sst, (ns / 3) & 1))
         issue_scores();
+    };
+    // y of chunk i, staged in the Q tile of stage t, whose tiles are released
+    // once it has been read
+    auto store = [&](int i, int t) {
+      if (y_tma && (i + 1) * C <= total && on && !*abort) {
+        unsigned char *d = sm + oKQ + t * kStageKQ + kHalf;
+        const int t_ = static_cast<int>(t0) + i * C;
+        tma_store_4d(&maps.y, d, p0, h, t_, b);
+        if (p0 + 64 < P) tma_store_4d(&maps.y, d + 2 * kHalf, p0 + 64, h, t_, b);
+      }
+    };
+    auto release = [&](int t) {
+      if (on) {
+        tma_store_wait_read();
+        mbar_arrive(bar + kEmptyKQ + t);
+      }
     };
     int st = 0;  // i % 3
     for (int i = 0; i < nc; ++i) {
@@ -383,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sy.wait(kReadyH, i & 1);
       tc_fence_after();
       if (alive()) {  // X = H K^T
-        const uint64_t dK = smem_desc(kq, 16, 1024);
+        const uint32_t dK = desc_lo(kq, 16);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
           const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
@@ -392,39 +499,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kDoneX, on);
-      try_scores();
-      const uint64_t dT = smem_desc(sbase + oT + (i & 1) * 2 * kHalf, 16, 1024);
-      sy.wait(kReadyT + (i & 1), (i / 2) & 1);
-      sy.wait(kFullV + (i & 1), (i / 2) & 1);
-      if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of the chunk before has been read
-      tc_fence_after();
-      if (alive()) {  // U^T = V^T T^T
-        const uint64_t dV = smem_desc(sbase + oV + (i & 1) * kStageV, kHalf, 1024);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mma_ss(kColU, dV + k * 128, dT + k * 2, idTK, k > 0, on);
-          mma_ss(kColU, dV + k * 128, dT + kLo + k * 2, idTK, 1, on);
-        }
-      }
-      mma_commit(bar + kEmptyV + (i & 1), on);
-      sy.wait(kReadyR, i & 1);
-      tc_fence_after();
-      if (alive()) {  // U^T += R^T T^T
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mma_ts(kColU, kColX + 16 * k, dT + k * 2, idKK, 1, on);
-          mma_ts(kColU, kColX + 16 * k + 8, dT + k * 2, idKK, 1, on);
-          mma_ts(kColU, kColX + 16 * k, dT + kLo + k * 2, idKK, 1, on);
-        }
-      }
-      mma_commit(bar + kDoneU, on);
-      try_scores();
       if (i > 0) {
         sy.wait(kFreeO, (i - 1) & 1);
         tc_fence_after();
+        store(i - 1, st == 0 ? 2 : st - 1);
       }
       if (alive()) {  // O1 = H Q^T
-        const uint64_t dQ = smem_desc(kq + kHalf, 16, 1024);
+        const uint32_t dQ = desc_lo(kq + kHalf, 16);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
           const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
@@ -434,22 +515,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(bar + kDoneO1, on);
       try_scores();
-      sy.wait(kReadyU, i & 1);
+      const uint32_t dT = desc_lo(sbase + oT + (i & 1) * 2 * kHalf, 16);
+      sy.wait(kReadyT + (i & 1), (i / 2) & 1);
+      sy.wait(kFullV + (i & 1), (i / 2) & 1);
+      if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of the chunk before has been read
+      tc_fence_after();
+      if (alive()) {  // U^T = V^T T^T
+        const uint32_t dV = desc_lo(sbase + oV, kHalf);
+#pragma unroll 2
+        for (int k = 0; k < 4; ++k) {
+          mma_ss(kColU, dV + k * 128, dT + k * 2, idTK, k > 0, on);
+          mma_ss(kColU, dV + k * 128, dT + kLo + k * 2, idTK, 1, on);
+        }
+      }
+      mma_commit(bar + kEmptyV, on);
+      sy.wait(kReadyR, i & 1);
+      tc_fence_after();
+      if (alive()) {  // U^T += R^T T^T
+#pragma unroll 2
+        for (int k = 0; k < 4; ++k) {
+          mma_ts(kColU, kColX + 16 * k, dT + k * 2, idKK, 1, on);
+          mma_ts(kColU, kColX + 16 * k + 8, dT + k * 2, idKK, 1, on);
+          mma_ts(kColU, kColX + 16 * k, dT + kLo + k * 2, idKK, 1, on);
+        }
+      }
+      mma_commit(bar + kDoneU, on);
+      try_scores();
       sy.wait(kDoneO1, i & 1);  // the update overwrites the pairs of H
+      sy.wait(kReadyU, i & 1);
       tc_fence_after();
       if (alive()) {  // U'^T K
-        const uint64_t dK = smem_desc(kq, 2 * kHalf, 1024);
-#pragma unroll
+        const uint32_t dK = desc_lo(kq, 2 * kHalf);
+#pragma unroll 2
         for (int k = 0; k < 4; ++k) {
           mma_ts(kColH, kColUd + 16 * k, dK + k * 128, idH, k > 0, on);
           mma_ts(kColH, kColUd + 16 * k + 8, dK + k * 128, idH, 1, on);
         }
       }
       mma_commit(bar + kDoneH, on);
-      mma_commit(bar + kEmptyKQ + st, on);
+      if (i > 0) release(st == 0 ? 2 : st - 1);
       if (alive()) {  // O2 = U^T (Q K^T o D)^T
-        const uint64_t dP = smem_desc(sbase + oP + (i & 1) * 2 * kHalf, 16, 1024);
-#pragma unroll
+        const uint32_t dP = desc_lo(sbase + oP + (i & 1) * 2 * kHalf, 16);
+#pragma unroll 2
         for (int k = 0; k < 4; ++k) {
           mma_ts(kColO2, kColU + 16 * k, dP + k * 2, idKK, k > 0, on);
           mma_ts(kColO2, kColU + 16 * k + 8, dP + k * 2, idKK, 1, on);
@@ -461,8 +568,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       try_scores();
       st = st == 2 ? 0 : st + 1;
     }
-    // every product done before the tensor memory is freed
-    if (nc > 0) sy.drain(kDoneO, (nc - 1) & 1);
+    // every product done before the tensor memory is freed, and every commit
+    // arrived, those too that nobody waits for: an arrival at the shared
+    // memory of a block that has ended is an illegal access
+    if (nc > 0) {
+      sy.drain(kDoneO, (nc - 1) & 1);
+      sy.drain(kEmptyV, (nc - 1) & 1);
+      sy.drain(kFreeP + ((nc - 1) & 1), ((nc - 1) / 2) & 1);
+      if (nc > 1) sy.drain(kFreeP + (nc & 1), ((nc - 2) / 2) & 1);
+      sy.wait(kFreeO, (nc - 1) & 1);
+      store(nc - 1, st == 0 ? 2 : st - 1);
+      tma_store_wait_all();
+    }
   } else if (warp == 2) {
     // --------------------------------------------------------- the gates
     const __nv_bfloat16 *dtp = static_cast<const __nv_bfloat16 *>(p.dt) + b * p.sdt[0] + h * p.sdt[2];
@@ -483,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (nc > 0) raw(0);
     for (int i = 0; i < nc; ++i) {
-      const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C;
+      const int left = total - i * C;
       float g2[2], bt[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -503,8 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           g2[1] += x1;
         }
       }
-      const float end0 = __shfl_sync(0xffffffffu, g2[0], 31);
-      g2[1] += end0;
+      g2[1] += __shfl_sync(0xffffffffu, g2[0], 31);
       const float end1 = __shfl_sync(0xffffffffu, g2[1], 31);
       if (i >= 2) sy.wait(kFreeG + (i & 1), (i / 2 - 1) & 1);
       if (i >= 3) sy.wait(kFreeD + i % 3, (i / 3 - 1) & 1);
@@ -520,7 +636,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         du[C + t] = eo;
         du[2 * C + t] = p.scale * eo;
       }
-      cum_s[C + lane] = ex2_mufu(end0 - g2[0]);
       warp_arrive(bar + kReadyG + i % 3, lane);
     }
   } else if (warp >= 4 && warp < 20) {
@@ -548,52 +663,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        uint32_t v[16];
-        tmem_ld16(tl + kColH + 32 * e + 16 * c, v);
-        tmem_wait_ld(v);
+        float v[16];
+        tmem_get16(tl + kColH + 32 * e + 16 * c, v);
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
           const float2 n = __ffma2_rn(make_float2(gam, gam),
                                       make_float2(H[16 * c + j], H[16 * c + j + 1]),
-                                      make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+                                      make_float2(v[j], v[j + 1]));
           H[16 * c + j] = n.x;
           H[16 * c + j + 1] = n.y;
         }
       }
     };
+    // column `row` of a 64-step tile in two halves of 64 columns: 16-byte
+    // chunk (row % 64) / 8 of a step's 128 bytes, swizzled by the step
+    const uint32_t ycol = (q >> 1) * 2 * kHalf + 2048 * e + (((32 * q + lane) & 63) << 1);
     // y rows of chunk i, 16 steps of a thread: scale 2^c O1 + O2 (P holds the
     // scale of O2)
     auto output = [&](int i) {
       sy.wait(kDoneO, i & 1);
       tc_fence_after();
       const float *eo = reinterpret_cast<const float *>(sm + oDecay + (i % 3) * kDecay) + 2 * C + 16 * e;
-      uint32_t v[16], w[16];
-      tmem_ld16(tl + kColO1 + 16 * e, v);
-      tmem_ld16(tl + kColO2 + 16 * e, w);
-      tmem_wait_ld(v);
-      tmem_wait_ld(w);
-      float o[16];
+      float v[16], o[16];
+      tmem_get16x2(tl + kColO1 + 16 * e, tl + kColO2 + 16 * e, v, o);
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        o[j] = fmaf(eo[j], __uint_as_float(v[j]), __uint_as_float(w[j]));
+      for (int j = 0; j < 16; j += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(eo + j);
+        o[j] = fmaf(x.x, v[j], o[j]);
+        o[j + 1] = fmaf(x.y, v[j + 1], o[j + 1]);
+        o[j + 2] = fmaf(x.z, v[j + 2], o[j + 2]);
+        o[j + 3] = fmaf(x.w, v[j + 3], o[j + 3]);
+      }
       tc_fence_before();
-      warp_arrive(bar + kFreeO, lane);
-      if (lane == 0) mbar_arrive(bar + kFreeD + i % 3);
-      const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C - 16 * e;
-      OutT *yr = yp + static_cast<int64_t>(i) * C * p.sy[1];
-      if (row < P) {
-        if (left >= 16) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) yr[j * p.sy[1]] = from_f32<OutT>(o[j]);
-        } else {
+      const int left = total - i * C - 16 * e;
+      if (y_tma && (i + 1) * C <= total) {
+        if constexpr (sizeof(OutT) == 2) {
+          unsigned char *d = sm + oKQ + (i % 3) * kStageKQ + kHalf;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (j < left) yr[j * p.sy[1]] = from_f32<OutT>(o[j]);
+            *reinterpret_cast<OutT *>(d + (ycol ^ ((j & 7) << 4)) + j * 128) = from_f32<OutT>(o[j]);
+          fence_async_smem();
         }
+      } else if (row < P) {
+        OutT *yr = yp + static_cast<int64_t>(i) * C * p.sy[1];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j < left) yr[j * p.sy[1]] = from_f32<OutT>(o[j]);
       }
+      warp_arrive(bar + kFreeO, lane);
+      if (lane == 0) mbar_arrive(bar + kFreeD + i % 3);
     };
-    for (int i = 0; i < nc; ++i) {
+    for (int i = 0;; ++i) {
       if (i > 0) update(i - 1);
+      if (i < nc) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t hi[8], lo[8];
@@ -605,32 +727,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(bar + kReadyH, lane);
+      }
+      if (i < nc) sy.wait(kReadyG + i % 3, (i / 3) & 1);
       if (i > 0) output(i - 1);
+      if (i >= nc) break;
 
       const float *du = reinterpret_cast<const float *>(sm + oDecay + (i % 3) * kDecay);
-      sy.wait(kReadyG + i % 3, (i / 3) & 1);
       sy.wait(kDoneX, i & 1);
       tc_fence_after();
       {
         // R = -2^c x, 16 steps of a thread, its pairs in the columns that x
         // came from; nothing of the steps behind the sequence
-        uint32_t x[16], hi[8], lo[8];
-        tmem_ld16(tl + kColX + 16 * e, x);
-        const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C - 16 * e;
+        float x[16];
+        uint32_t hi[8], lo[8];
+        const int left = total - i * C - 16 * e;
         const float *ec = du + C + 16 * e;
-        tmem_wait_ld(x);
+        tmem_get16(tl + kColX + 16 * e, x);
         if (left < 16) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (j >= left) x[j] = 0u;
+            if (j >= left) x[j] = 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 w = *reinterpret_cast<const float4 *>(ec + j);
-          split2(-w.x * __uint_as_float(x[j]), -w.y * __uint_as_float(x[j + 1]), hi[j / 2],
-                 lo[j / 2]);
-          split2(-w.z * __uint_as_float(x[j + 2]), -w.w * __uint_as_float(x[j + 3]),
-                 hi[j / 2 + 1], lo[j / 2 + 1]);
+          split2(-w.x * x[j], -w.y * x[j + 1], hi[j / 2], lo[j / 2]);
+          split2(-w.z * x[j + 2], -w.w * x[j + 3], hi[j / 2 + 1], lo[j / 2 + 1]);
         }
         tmem_st8(tl + kColX + 16 * e, hi);
         tmem_st8(tl + kColX + 16 * e + 8, lo);
@@ -643,31 +765,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       gam = du[2 * C - 1];
       tc_fence_after();
       {
-        uint32_t v[16], hi[8], lo[8];
-        tmem_ld16(tl + kColU + 16 * e, v);
-        tmem_wait_ld(v);
+        float v[16];
+        uint32_t hi[8], lo[8];
+        tmem_get16(tl + kColU + 16 * e, v);
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 d = *reinterpret_cast<const float4 *>(du + 16 * e + j);
-          split2(__uint_as_float(v[j]) * d.x, __uint_as_float(v[j + 1]) * d.y, hi[j / 2], lo[j / 2]);
-          split2(__uint_as_float(v[j + 2]) * d.z, __uint_as_float(v[j + 3]) * d.w, hi[j / 2 + 1],
-                 lo[j / 2 + 1]);
+          split2(v[j] * d.x, v[j + 1] * d.y, hi[j / 2], lo[j / 2]);
+          split2(v[j + 2] * d.z, v[j + 3] * d.w, hi[j / 2 + 1], lo[j / 2 + 1]);
         }
         tmem_st8(tl + kColUd + 16 * e, hi);
         tmem_st8(tl + kColUd + 16 * e + 8, lo);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          split2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]), hi[j], lo[j]);
+        for (int j = 0; j < 8; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
         tmem_st8(tl + kColU + 16 * e, hi);
         tmem_st8(tl + kColU + 16 * e + 8, lo);
       }
       tmem_wait_st();
       tc_fence_before();
       warp_arrive(bar + kReadyU, lane);
-    }
-    if (nc > 0) {
-      update(nc - 1);
-      output(nc - 1);
     }
     if (p.last && row < P) {
 #pragma unroll
@@ -678,119 +794,106 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 20) {
     // ------------------------------------- what does not depend on H
-    const int q = warp & 3, e = (warp - 20) >> 2, at = tid - 640, aw = warp - 20;
+    // group gr takes the chunks of its parity
+    const int q = warp & 3, gr = (warp - 20) >> 2, at = tid - 640 - gr * kAux, aw = at >> 5;
     const uint32_t tl = static_cast<uint32_t>(32 * q) << 16;
-    float *scr = reinterpret_cast<float *>(sm + oScr);
+    float *scr = reinterpret_cast<float *>(sm + oScr) + gr * 4 * kBlk;
+    unsigned char *pt = sm + oP + gr * 2 * kHalf, *tt = sm + oT + gr * 2 * kHalf;
+    const float *beta_s = reinterpret_cast<const float *>(sm + oGate + gr * kGate);
+    const float *cum_s = beta_s + C;
 
-    // the blocks of P and T above the diagonal stay zero, and so does that of
-    // the two 32 x 32 inverses
-    for (int k = at; k < 8 * 32 * 4; k += kAux)
-      *reinterpret_cast<uint4 *>(sm + oP + (k >> 7) * kHalf + swz((k >> 2) & 31, 4 + (k & 3))) =
-          make_uint4(0u, 0u, 0u, 0u);
-    for (int k = at; k < 2 * 16 * 16; k += kAux)
-      scr[(k < 256 ? bT11 : bT22) * kBlk + ((k >> 4) & 15) * kLd + 16 + (k & 15)] = 0.f;
-    bar_sync(kBarAux, kAux);
+    // the blocks of P and T above the diagonal stay zero
+    for (int k = at; k < 4 * 32 * 4; k += kAux)
+      *reinterpret_cast<uint4 *>((k < 256 ? pt : tt) + ((k >> 7) & 1) * kHalf +
+                                 swz((k >> 2) & 31, 4 + (k & 3))) = make_uint4(0u, 0u, 0u, 0u);
 
-    int st = 0;  // i % 3
-    for (int i = 0; i < nc; ++i, st = st == 2 ? 0 : st + 1) {
-      const int64_t left = t1 - t0 - static_cast<int64_t>(i) * C;
-      const int len = left < C ? static_cast<int>(left) : C;
-      const float *beta_s = reinterpret_cast<const float *>(sm + oGate + (i & 1) * kGate);
-      const float *cum_s = beta_s + C, *colf_s = cum_s + C;
-      const float *du = reinterpret_cast<const float *>(sm + oDecay + st * kDecay);
-      unsigned char *tt = sm + oT + (i & 1) * 2 * kHalf;
+    for (int i = gr; i < nc; i += 2) {
+      const int st = i % 3;
+      const int len = min(total - i * C, C);
       sy.wait(kReadyG + st, (i / 3) & 1);
-      sy.wait(kDoneS, i & 1);
-      if (i >= 2) {  // the buffers that U and O2 of chunk i - 2 read
-        sy.wait(kFreeP + (i & 1), (i / 2 - 1) & 1);
-      }
+      sy.wait(kDoneS + gr, (i / 2) & 1);
+      // the buffers that U and O2 of chunk i - 2 read
+      if (i >= 2) sy.wait(kFreeP + gr, (i / 2 - 1) & 1);
       tc_fence_after();
 
       if (len < C) {
         // keys and values of whatever lies behind the sequence: nothing of
         // them may enter a product over steps (zero times a NaN would)
         sy.wait(kFullKQ + st, (i / 3) & 1);
-        sy.wait(kFullV + (i & 1), (i / 2) & 1);
+        sy.wait(kFullV + gr, (i / 2) & 1);
         const int rows = C - len;
         for (int k = at; k < rows * 32; k += kAux) {
           const int r = len + (k >> 5), c = k & 31;
           unsigned char *d = c < 16 ? sm + oKQ + st * kStageKQ + (c >> 3) * 2 * kHalf
-                                    : sm + oV + (i & 1) * kStageV + ((c >> 3) & 1) * kHalf;
+                                    : sm + oV + ((c >> 3) & 1) * kHalf;
           *reinterpret_cast<uint4 *>(d + r * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
 
-      // rows of A (lanes 0..63 of S) and of scale Q K^T o D (64..127), 32 columns
-      // of a thread: below the diagonal 2^(c_t - c_end) 2^(c_end - c_s),
-      // c_end the end of s's block of 32, both at most 1; in a diagonal block
-      // the same two factors unless the first could overflow, else one 2^x
-      // each
-      const int blk = q & 1;
-      const bool diag = e == blk, isA = q < 2;
-      if (e <= blk) {
-        const int t = 32 * blk + lane;
-        const float cend = cum_s[32 * e + 31], ct = cum_s[t];
-        const float rowf = isA ? beta_s[t] : p.scale;
-        const bool fact = !diag || cum_s[32 * e] - cend < 64.0f;
-        const float rf = rowf * ex2_mufu(ct - cend);
-        const float *cf = e ? du + 32 : colf_s;
+      // rows of A (lanes 0..63 of S) and of scale Q K^T o D (64..127) in
+      // blocks of 32 columns, the diagonal one first, 16 columns at a time
+      const int blk = q & 1, t = 32 * blk + lane;
+      const bool isA = q < 2;
+      const float ct = cum_s[t], rowf = isA ? beta_s[t] : p.scale;
+#pragma unroll 1
+      for (int part = 0; part <= 2 * blk + 1; ++part) {
+        const bool diag = part < 2;
+        const int e = diag ? blk : 0, c = part & 1;
         // columns kept
-        const int last = t >= len ? 0 : (diag ? (isA ? lane : lane + 1) : 32);
-        unsigned char *d = sm + oP + (i & 1) * 2 * kHalf;
-        float *da = scr + (diag ? (blk ? bA22 : bA11) : bA21) * kBlk + lane;
+        const int last = t >= len ? 0 : (diag ? (isA ? lane : lane + 1) - 16 * c : 16);
+        const float *cs = cum_s + 32 * e + 16 * c;
+        float v[16], f[16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t v[16];
-          float f[16];
-          tmem_ld16(tl + kColS + 32 * e + 16 * c, v);
-          if (fact) {
+        for (int j = 0; j < 16; j += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(cs + j);
+          f[j] = ex2_mufu(ct - x.x);
+          f[j + 1] = ex2_mufu(ct - x.y);
+          f[j + 2] = ex2_mufu(ct - x.z);
+          f[j + 3] = ex2_mufu(ct - x.w);
+        }
+        tmem_get16(tl + kColS + 32 * e + 16 * c, v);
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 x = *reinterpret_cast<const float4 *>(cf + 16 * c + j);
-              f[j] = rf * x.x;
-              f[j + 1] = rf * x.y;
-              f[j + 2] = rf * x.z;
-              f[j + 3] = rf * x.w;
-            }
-          } else {
+        for (int j = 0; j < 16; j += 2) {
+          const float2 y =
+              __fmul2_rn(make_float2(f[j], f[j + 1]),
+                         __fmul2_rn(make_float2(rowf, rowf), make_float2(v[j], v[j + 1])));
+          f[j] = j < last ? y.x : 0.f;
+          f[j + 1] = j + 1 < last ? y.y : 0.f;
+        }
+        if (isA) {  // transposed: the substitution reads columns of A
+          float *da = scr + (diag ? (blk ? bA22 : bA11) : bA21) * kBlk + lane + 16 * c * kLd;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = rowf * ex2_mufu(ct - cum_s[32 * e + 16 * c + j]);
-          }
-          tmem_wait_ld(v);
+          for (int j = 0; j < 16; ++j) da[j * kLd] = f[j];
+        } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            f[j] = 16 * c + j < last ? f[j] * __uint_as_float(v[j]) : 0.f;
-          if (isA) {  // transposed: the substitution reads columns of A
-#pragma unroll
-            for (int j = 0; j < 16; ++j) da[(16 * c + j) * kLd] = f[j];
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint4 hi, lo;
-              split8(f + 8 * k, hi, lo);
-              const uint32_t o = swz(t, 4 * e + 2 * c + k);
-              *reinterpret_cast<uint4 *>(d + o) = hi;
-              *reinterpret_cast<uint4 *>(d + kHalf + o) = lo;
-            }
+          for (int k = 0; k < 2; ++k) {
+            uint4 hi, lo;
+            split8(f + 8 * k, hi, lo);
+            const uint32_t o = swz(t, 4 * e + 2 * c + k);
+            *reinterpret_cast<uint4 *>(pt + o) = hi;
+            *reinterpret_cast<uint4 *>(pt + kHalf + o) = lo;
           }
         }
+        // A22 is there for the warp of q = 2
+        if (q == 1 && part == 1) bar_arrive(kBarA22 + gr, 64);
       }
       tc_fence_before();
       warp_arrive(bar + kFreeS, lane);
-      // the warps of the two diagonal blocks of A invert them
-      if (isA && diag)
-        invert32(scr + (blk ? bA22 : bA11) * kBlk, scr + (blk ? bT22 : bT11) * kBlk,
-                 scr + bZ * kBlk + blk * 16 * kLd, lane);
-      bar_sync(kBarAux, kAux);
-      // T21 = -T22 (A21 T11)
-      const int r0 = 16 * (aw >> 2), n0 = 8 * (aw & 3);
-      float z[4];
-      tile<32>(scr + bA21 * kBlk + r0, 1, kLd, scr + bT11 * kBlk + n0, lane, z);
-      store_tile(scr + bZ * kBlk + r0 * kLd + n0, lane, z, 1.f);
-      {
+      if (!blk) {
+        if (q) bar_sync(kBarA22 + gr, 64);
+        invert32(scr + (q ? bA22 : bA11) * kBlk, lane);
+      }
+      bar_sync(kBarAux + gr, kAux);
+      // T21 = -T22 (A21 T11), a 16 x 16 block of a warp
+      const int r0 = 16 * (aw >> 1), n0 = 16 * (aw & 1);
+      float z[2][4];
+      tiles<32>(scr + bA21 * kBlk + r0, 1, kLd, scr + bA11 * kBlk + n0, lane, z);
+      store_tiles(scr + bZ * kBlk + r0 * kLd + n0, lane, z, 1.f);
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
         // pairs of T11 and T22, times b: 8 columns of a row
-        const int w = at >> 7, r = (at >> 2) & 31, c = at & 3;
-        const float *src = scr + (w ? bT22 : bT11) * kBlk + r * kLd + 8 * c;
+        const int r = at >> 2, c = at & 3;
+        const float *src = scr + (w ? bA22 : bA11) * kBlk + r * kLd + 8 * c;
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; j += 4) {
@@ -807,28 +910,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(tt + o) = hi;
         *reinterpret_cast<uint4 *>(tt + kHalf + o) = lo;
       }
-      bar_sync(kBarAux, kAux);
-      const float2 nb = *reinterpret_cast<const float2 *>(beta_s + n0 + 2 * (lane & 3));
-      tile<32>(scr + bT22 * kBlk + r0 * kLd, kLd, 1, scr + bZ * kBlk + n0, lane, z);
+      bar_sync(kBarAux + gr, kAux);
+      tiles<32>(scr + bA22 * kBlk + r0 * kLd, kLd, 1, scr + bZ * kBlk + n0, lane, z);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t hi, lo;
-        split2(-z[2 * k] * nb.x, -z[2 * k + 1] * nb.y, hi, lo);
-        const uint32_t o = swz(32 + r0 + 8 * k + (lane >> 2), aw & 3) + 4 * (lane & 3);
-        *reinterpret_cast<uint32_t *>(tt + o) = hi;
-        *reinterpret_cast<uint32_t *>(tt + kHalf + o) = lo;
+      for (int n = 0; n < 2; ++n) {
+        const int c = n0 + 8 * n + 2 * (lane & 3);
+        const float2 nb = *reinterpret_cast<const float2 *>(beta_s + c);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t hi, lo;
+          split2(-z[n][2 * k] * nb.x, -z[n][2 * k + 1] * nb.y, hi, lo);
+          const uint32_t o = swz(32 + r0 + 8 * k + (lane >> 2), c >> 3) + 4 * (lane & 3);
+          *reinterpret_cast<uint32_t *>(tt + o) = hi;
+          *reinterpret_cast<uint32_t *>(tt + kHalf + o) = lo;
+        }
       }
       fence_async_smem();
-      warp_arrive(bar + kReadyT + (i & 1), lane);
-      if (lane == 0) mbar_arrive(bar + kFreeG + (i & 1));
-      // (the next chunk's A overwrites what the last product read: the
-      // barrier after its inverses comes too late for that)
-      bar_sync(kBarAux, kAux);
+      warp_arrive(bar + kReadyT + gr, lane);
+      if (lane == 0) mbar_arrive(bar + kFreeG + gr);
+      // (the next chunk's A overwrites what the last product read)
+      bar_sync(kBarAux + gr, kAux);
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort) atomicOr(p.status, static_cast<unsigned>(MSS_ERR_TIMEOUT));
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(*tmem_slot, kTmemCols);
@@ -888,13 +995,16 @@ cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t
       !encode(&maps.k, p.k, p.N, p.G, p.L, p.batch, p.sk) ||
       !encode(&maps.v, p.v, p.P, p.H, p.L, p.batch, p.sv))
     return cudaErrorInvalidValue;
+  // y through tensor maps: bf16, rows on 16-byte boundaries
+  const int y_tma = out_bf16 && al16(p.y) && map_strides(p.sy, p.batch, p.L, p.H) &&
+                    encode(&maps.y, p.y, p.P, p.H, p.L, p.batch, p.sy);
   const unsigned grid = static_cast<unsigned>(p.seqs * p.H * ((p.P + 127) / 128));
   auto run = [&](auto kernel) {
     // per launch: the attribute belongs to the current device
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, kSmemBytes, stream>>>(maps, p);
+    kernel<<<grid, kThreads, kSmemBytes, stream>>>(maps, p, y_tma);
     return cudaGetLastError();
   };
   if (p.N <= 64)
