@@ -355,9 +355,9 @@ __device__ __forceinline__ void invert32(float *a, int lane) {
 }
 
 // NK: 16-wide slices of dstate (4 up to 64, else 8; TMA pads with zeros).
-// y_tma: whole chunks of y go out through the Q tile of their stage and a TMA
-// store (bf16 rows that a tensor map takes): 16 two-byte stores of a thread
-// straight to memory took 1.3 us of a chunk's 4.5.
+// y_tma: whole chunks of y go out through their Q tile, which has been read by
+// then, and a TMA store (bf16 rows that a tensor map takes): 16 two-byte
+// stores of a thread straight to memory took 1.3 us of a chunk's 4.5.
 template <typename OutT, int NK>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p, const int y_tma) {
@@ -463,14 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ns < nc && (ns == 0 || ready(kFreeS, (ns - 1) & 1)) && ready(kFullKQ + sst, (ns / 3) & 1))
         issue_scores();
     };
-    // y of chunk i, staged in the Q tile of stage t, whose tiles are released
+    // y of chunk i, staged in the Q tile of its stage t, which is released
     // once it has been read
     auto store = [&](int i, int t) {
       if (y_tma && (i + 1) * C <= total && on && !*abort) {
         unsigned char *d = sm + oKQ + t * kStageKQ + kHalf;
-        const int t_ = static_cast<int>(t0) + i * C;
-        tma_store_4d(&maps.y, d, p0, h, t_, b);
-        if (p0 + 64 < P) tma_store_4d(&maps.y, d + 2 * kHalf, p0 + 64, h, t_, b);
+        const int step = static_cast<int>(t0) + i * C;
+        tma_store_4d(&maps.y, d, p0, h, step, b);
+        if (p0 + 64 < P) tma_store_4d(&maps.y, d + 2 * kHalf, p0 + 64, h, step, b);
       }
     };
     auto release = [&](int t) {
@@ -499,6 +499,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kDoneX, on);
+      const uint32_t dT = desc_lo(sbase + oT + (i & 1) * 2 * kHalf, 16);
+      sy.wait(kReadyT + (i & 1), (i / 2) & 1);
+      sy.wait(kFullV + (i & 1), (i / 2) & 1);
+      if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of the chunk before has been read
+      tc_fence_after();
+      if (alive()) {  // U^T = V^T T^T
+        const uint32_t dV = desc_lo(sbase + oV, kHalf);
+#pragma unroll 2
+        for (int k = 0; k < 4; ++k) {
+          mma_ss(kColU, dV + k * 128, dT + k * 2, idTK, k > 0, on);
+          mma_ss(kColU, dV + k * 128, dT + kLo + k * 2, idTK, 1, on);
+        }
+      }
+      mma_commit(bar + kEmptyV, on);
       if (i > 0) {
         sy.wait(kFreeO, (i - 1) & 1);
         tc_fence_after();
@@ -515,20 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(bar + kDoneO1, on);
       try_scores();
-      const uint32_t dT = desc_lo(sbase + oT + (i & 1) * 2 * kHalf, 16);
-      sy.wait(kReadyT + (i & 1), (i / 2) & 1);
-      sy.wait(kFullV + (i & 1), (i / 2) & 1);
-      if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of the chunk before has been read
-      tc_fence_after();
-      if (alive()) {  // U^T = V^T T^T
-        const uint32_t dV = desc_lo(sbase + oV, kHalf);
-#pragma unroll 2
-        for (int k = 0; k < 4; ++k) {
-          mma_ss(kColU, dV + k * 128, dT + k * 2, idTK, k > 0, on);
-          mma_ss(kColU, dV + k * 128, dT + kLo + k * 2, idTK, 1, on);
-        }
-      }
-      mma_commit(bar + kEmptyV, on);
+      if (i > 0) release(st == 0 ? 2 : st - 1);
       sy.wait(kReadyR, i & 1);
       tc_fence_after();
       if (alive()) {  // U^T += R^T T^T
@@ -553,7 +554,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kDoneH, on);
-      if (i > 0) release(st == 0 ? 2 : st - 1);
       if (alive()) {  // O2 = U^T (Q K^T o D)^T
         const uint32_t dP = desc_lo(sbase + oP + (i & 1) * 2 * kHalf, 16);
 #pragma unroll 2
@@ -574,8 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nc > 0) {
       sy.drain(kDoneO, (nc - 1) & 1);
       sy.drain(kEmptyV, (nc - 1) & 1);
-      sy.drain(kFreeP + ((nc - 1) & 1), ((nc - 1) / 2) & 1);
-      if (nc > 1) sy.drain(kFreeP + (nc & 1), ((nc - 2) / 2) & 1);
+      for (int i = nc > 2 ? nc - 2 : 0; i < nc; ++i) sy.drain(kFreeP + (i & 1), (i / 2) & 1);
       sy.wait(kFreeO, (nc - 1) & 1);
       store(nc - 1, st == 0 ? 2 : st - 1);
       tma_store_wait_all();
@@ -812,8 +811,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int len = min(total - i * C, C);
       sy.wait(kReadyG + st, (i / 3) & 1);
       sy.wait(kDoneS + gr, (i / 2) & 1);
-      // the buffers that U and O2 of chunk i - 2 read
-      if (i >= 2) sy.wait(kFreeP + gr, (i / 2 - 1) & 1);
       tc_fence_after();
 
       if (len < C) {
@@ -835,6 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int blk = q & 1, t = 32 * blk + lane;
       const bool isA = q < 2;
       const float ct = cum_s[t], rowf = isA ? beta_s[t] : p.scale;
+      // U and O2 of chunk i - 2 have read the T and P in this one's place (the
+      // other warps write T behind a barrier with these)
+      if (!isA && i >= 2) sy.wait(kFreeP + gr, (i / 2 - 1) & 1);
 #pragma unroll 1
       for (int part = 0; part <= 2 * blk + 1; ++part) {
         const bool diag = part < 2;
