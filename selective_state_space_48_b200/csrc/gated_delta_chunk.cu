@@ -29,17 +29,20 @@
 // is added to there, not in the tensor cores' accumulators.
 //
 // Roles (28 warps, one block per SM: the sequence, head and 128 rows):
-//   warps 0, 3    TMA loads of the K, Q tiles (three stages); of V (one)
-//   warp 1        issues every product
+//   warps 0, 3    TMA loads of the K, Q tiles (three stages); of V (one), and
+//                 the stores of y
+//   warp 1        issues every product, those that are not on the chain in the
+//                 shadow of its other work
 //   warp 2        the gates: running sums of log2 a and what follows from them
 //   warps 4-19    the chain: H in registers (32 columns a thread), its pairs
-//                 and those of R and U into tensor memory; the output, while
-//                 the next product with H runs
+//                 and those of R and U into tensor memory; the output of the
+//                 chunk before, while products run
 //   warps 20-27   what does not depend on H: A, its inverse T, Q K^T o D; two
 //                 groups of four that take chunks in turn, since a chunk takes
 //                 them longer than the chain takes for one
 // The inverse: 16 x 16 triangles by substitution, a column per lane, then the
-// blocks below them as products, -T22 (A21 T11), in 3 x tf32 mma.sync.
+// blocks below them as products, -T22 (A21 T11), in fp32 (2 x 4 values of a
+// thread; the same as three tf32 mma.sync products took 2.2 us more of a chunk).
 //
 // Shared memory tiles are rows of 128 bytes with the 128-byte swizzle.  Every
 // wait is bounded as in tcgen05.cuh, so no block can hang.
@@ -70,13 +73,13 @@ constexpr int oScr = oT + 4 * kHalf;  // scratch of the inverse, for each group
 // 32 x 32 blocks, rows of 40 floats (8 rows start on 8 groups of banks): A,
 // transposed, then T in the diagonal ones; A21 T11
 constexpr int kLd = 40, kBlk = 32 * kLd;
-constexpr int bA11 = 0, bA22 = 1, bA21 = 2, bZ = 3;
-constexpr int oGate = oScr + 2 * 4 * kBlk * 4;  // two of (b, c) [C]
+constexpr int bA11 = 0, bA22 = 1, bA21 = 2, bZ = 3, kScr = 4 * kBlk;
+constexpr int oGate = oScr + 2 * kScr * 4;  // two of (b, c) [C]
 constexpr int kGate = 2 * C * 4;
 constexpr int oDecay = oGate + 2 * kGate;  // three of (2^(c_last - c), 2^c, scale 2^c) [C]
 constexpr int kDecay = 3 * C * 4;
 constexpr int oBar = oDecay + 3 * kDecay;
-constexpr int kBars = 33;
+constexpr int kBars = 34;
 constexpr int oTmemSlot = oBar + kBars * 8;
 constexpr int oAbort = oTmemSlot + 4;
 constexpr int kSmemBytes = oAbort + 4;
@@ -85,28 +88,28 @@ static_assert(oGate % 16 == 0 && kGate % 16 == 0 && oDecay % 16 == 0, "16-byte v
 
 // tensor memory columns (all 512 are allocated, so they start at 0)
 constexpr uint32_t kColH = 0;     // H pairs / the update U'^T K (128)
-constexpr uint32_t kColX = 128;   // H K^T, then the pairs of R
+constexpr uint32_t kColX = 128;   // H K^T, then the pairs of R, then those of
+                                  // U' = U diag(2^(c_last - c))
 constexpr uint32_t kColU = 192;   // U, then its pairs
-constexpr uint32_t kColUd = 256;  // pairs of U' = U diag(2^(c_last - c))
-constexpr uint32_t kColO1 = 320, kColO2 = 384;
+constexpr uint32_t kColO1 = 256;  // two
+constexpr uint32_t kColO2 = 384;
 constexpr uint32_t kColS = 448;   // K K^T (lanes 0..63), Q K^T (64..127)
 constexpr uint32_t kTmemCols = 512;
 
-// Barriers.  Tiles landed and released; per chunk, products done (S, X, U,
-// O1, the update, O) and operands ready (H; R; U; T and P), S and O drained;
-// the two T and P buffers released; the gates written (the decays have three
-// buffers, the rest two) and their two and three buffers released.  A waiter may not fall two phases
-// behind: where it could, the barriers are a ring.  The groups arrive one
-// lane per warp.
+// Barriers.  Tiles landed and released; per chunk, products done (S, X, U, O1,
+// the update, O) and operands ready (H; R; U; T and P), S and O drained; y staged; the two P buffers released; the gates written (the decays have three buffers, the rest
+// two) and their two and three buffers released.  A waiter may not fall two
+// phases behind: where it could, the barriers are a ring.  The groups arrive
+// one lane per warp.
 constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 9, kDoneX = 11,
               kDoneU = 12, kDoneO1 = 13, kDoneH = 14, kDoneO = 15, kReadyH = 16, kReadyR = 17,
-              kReadyU = 18, kFreeO = 19, kFreeS = 20, kReadyT = 21, kFreeP = 23, kReadyG = 25,
-              kFreeG = 28, kFreeD = 30;  // .. 32
+              kReadyU = 18, kFreeO = 19, kReadyY = 20, kFreeS = 21, kReadyT = 22, kFreeP = 24,
+              kReadyG = 26, kFreeG = 29, kFreeD = 31;  // .. 33
 // arrivals that complete a barrier's phase
 __device__ __forceinline__ int bar_count(int i) {
   if (i == kFreeS || i == kReadyT || i == kReadyT + 1 || i == kFreeG || i == kFreeG + 1)
     return kAuxWarps;
-  if ((i >= kReadyH && i <= kFreeO) || i >= kFreeD)
+  if ((i >= kReadyH && i <= kReadyY) || i >= kFreeD)
     return kChainWarps;
   return 1;
 }
@@ -259,57 +262,45 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t go) {
       : "memory");
 }
 
-// c += a b, m16n8k8, tf32 operands (bits below tf32's are not read)
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4],
-                                         const uint32_t (&b)[2]) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9},"
-      " {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+// z += x y for two rows of four columns
+__device__ __forceinline__ void fma24(float2 (&z)[2][2], float x0, float x1, float4 y) {
+  z[0][0] = __ffma2_rn(make_float2(x0, x0), make_float2(y.x, y.y), z[0][0]);
+  z[0][1] = __ffma2_rn(make_float2(x0, x0), make_float2(y.z, y.w), z[0][1]);
+  z[1][0] = __ffma2_rn(make_float2(x1, x1), make_float2(y.x, y.y), z[1][0]);
+  z[1][1] = __ffma2_rn(make_float2(x1, x1), make_float2(y.z, y.w), z[1][1]);
 }
-__device__ __forceinline__ void split_tf32(float x, uint32_t &hi, uint32_t &lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
-}
-
-// Two neighbouring 16 x 8 tiles of X Y, DEPTH deep, as three tf32 products
-// each; X[r][k] at xa + r * xr + k * xk, Y[k][n] at yb + k * kLd + n.  A lane
-// gets rows lane / 4 and lane / 4 + 8, columns 2 (lane % 4) and the next of
-// either tile.
+// Rows r, r + 1, columns c .. c + 3 of X Y, DEPTH deep: X given transposed (x
+// points to its row r of values r, y to columns c), ...
 template <int DEPTH>
-__device__ __forceinline__ void tiles(const float *xa, int xr, int xk, const float *yb, int lane,
-                                      float (&out)[2][4]) {
-  const int g = lane >> 2, t = lane & 3;
-  float c0[2][4] = {}, c1[2][4] = {}, c2[2][4] = {};
-#pragma unroll 2
-  for (int k = 0; k < DEPTH; k += 8) {
-    uint32_t ah[4], al[4], bh[2], bl[2];
+__device__ __forceinline__ void prod_t(const float *x, const float *y, float2 (&z)[2][2]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      split_tf32(xa[(g + 8 * (i & 1)) * xr + (k + t + 4 * (i >> 1)) * xk], ah[i], al[i]);
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) split_tf32(yb[(k + t + 4 * i) * kLd + 8 * n + g], bh[i], bl[i]);
-      mma_tf32(c0[n], ah, bh);
-      mma_tf32(c1[n], al, bh);
-      mma_tf32(c2[n], ah, bl);
-    }
+  for (int i = 0; i < 4; ++i) z[i >> 1][i & 1] = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int k = 0; k < DEPTH; ++k) {
+    const float2 v = *reinterpret_cast<const float2 *>(x + k * kLd);
+    fma24(z, v.x, v.y, *reinterpret_cast<const float4 *>(y + k * kLd));
   }
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[n][i] = c0[n][i] + (c1[n][i] + c2[n][i]);
 }
-__device__ __forceinline__ void store_tiles(float *d, int lane, const float (&z)[2][4],
-                                            float sign) {
-  d += (lane >> 2) * kLd + 2 * (lane & 3);
+// ... or as it is (x points to its row r)
+template <int DEPTH>
+__device__ __forceinline__ void prod_n(const float *x, const float *y, float2 (&z)[2][2]) {
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    *reinterpret_cast<float2 *>(d + 8 * n) = make_float2(sign * z[n][0], sign * z[n][1]);
-    *reinterpret_cast<float2 *>(d + 8 * kLd + 8 * n) = make_float2(sign * z[n][2], sign * z[n][3]);
+  for (int i = 0; i < 4; ++i) z[i >> 1][i & 1] = make_float2(0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < DEPTH; k += 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(x + k);
+    const float4 w = *reinterpret_cast<const float4 *>(x + kLd + k);
+    fma24(z, v.x, w.x, *reinterpret_cast<const float4 *>(y + k * kLd));
+    fma24(z, v.y, w.y, *reinterpret_cast<const float4 *>(y + (k + 1) * kLd));
+    fma24(z, v.z, w.z, *reinterpret_cast<const float4 *>(y + (k + 2) * kLd));
+    fma24(z, v.w, w.w, *reinterpret_cast<const float4 *>(y + (k + 3) * kLd));
   }
+}
+__device__ __forceinline__ void store24(float *d, const float2 (&z)[2][2], float sign) {
+  *reinterpret_cast<float4 *>(d) =
+      make_float4(sign * z[0][0].x, sign * z[0][0].y, sign * z[0][1].x, sign * z[0][1].y);
+  *reinterpret_cast<float4 *>(d + kLd) =
+      make_float4(sign * z[1][0].x, sign * z[1][0].y, sign * z[1][1].x, sign * z[1][1].y);
 }
 
 // (I + A)^-1 of a 32 x 32 block in place, by one warp; `a` holds A transposed
@@ -341,26 +332,35 @@ __device__ __forceinline__ void invert32(float *a, int lane) {
     }
   }
   __syncwarp();
-  float z[2][4];
-  tiles<16>(a + 16, 1, kLd, a, lane, z);
-  store_tiles(a + 16 * kLd, lane, z, 1.f);
+  const int r = 2 * (lane >> 2), c = 4 * (lane & 3);
+  float2 z[2][2];
+  prod_t<16>(a + 16 + r, a + c, z);
+  store24(a + (16 + r) * kLd + c, z, 1.f);
   __syncwarp();
-  tiles<16>(a + 16 * kLd + 16, kLd, 1, a + 16 * kLd, lane, z);
+  prod_n<16>(a + (16 + r) * kLd + 16, a + 16 * kLd + c, z);
 #pragma unroll
   for (int i = 0; i < 2; ++i)  // above the diagonal T is zero
     *reinterpret_cast<float4 *>(a + (lane >> 1) * kLd + 16 + 8 * (lane & 1) + 4 * i) =
         make_float4(0.f, 0.f, 0.f, 0.f);
   __syncwarp();
-  store_tiles(a + 16 * kLd, lane, z, -1.f);
+  store24(a + (16 + r) * kLd + c, z, -1.f);
+}
+
+constexpr uint32_t kIdKK = idesc_bf16(128, 64, 0, 0);  // both operands K-major
+constexpr uint32_t kIdTK = idesc_bf16(128, 64, 1, 0);  // the first as stored by step
+constexpr uint32_t kLoTile = kHalf >> 4;               // hi -> lo of T and P
+// slice k of a K-major tile whose 64-wide halves lie 2 kHalf apart
+__device__ __forceinline__ constexpr uint32_t kslice(int k) {
+  return static_cast<uint32_t>((k >> 2) * (2 * kHalf >> 4) + (k & 3) * 2);
 }
 
 // NK: 16-wide slices of dstate (4 up to 64, else 8; TMA pads with zeros).
-// y_tma: whole chunks of y go out through their Q tile, which has been read by
-// then, and a TMA store (bf16 rows that a tensor map takes): 16 two-byte
+// y_tma: whole chunks of y go out through their Q tile and a TMA store (bf16 rows that a tensor map takes): 16 two-byte
 // stores of a thread straight to memory took 1.3 us of a chunk's 4.5.
 template <typename OutT, int NK>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p, const int y_tma) {
+  constexpr uint32_t idH = idesc_bf16(128, 16 * NK, 0, 1);  // the second as stored by step
   // the swizzle needs 1024-byte tiles; a block without static shared memory
   // has its dynamic memory on such a boundary
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -419,28 +419,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 3) {
-    // (a producer of its own: V waits for its one place, K and Q run ahead)
+    // (V waits for its one place, while K and Q run ahead)
     if (lane == 0) {
-      for (int i = 0; i < nc; ++i) {
-        if (i >= 1) sy.wait(kEmptyV, (i - 1) & 1);
-        const int t = static_cast<int>(t0) + i * C;
-        uint64_t *full = bar + kFullV + (i & 1);
-        mbar_expect_tx(full, kStageV);
-        tma_load_4d(sm + oV, &maps.v, p0, h, t, b, full);
-        tma_load_4d(sm + oV + kHalf, &maps.v, p0 + 64, h, t, b, full);
+      for (int i = 0; i <= nc; ++i) {
+        if (i > 0) sy.wait(kEmptyV, (i - 1) & 1);
+        if (i < nc) {
+          const int t = static_cast<int>(t0) + i * C;
+          uint64_t *full = bar + kFullV + (i & 1);
+          mbar_expect_tx(full, kStageV);
+          tma_load_4d(sm + oV, &maps.v, p0, h, t, b, full);
+          tma_load_4d(sm + oV + kHalf, &maps.v, p0 + 64, h, t, b, full);
+        }
+        if (i == 0 || !y_tma || i * C > total) continue;
+        // y of chunk i - 1, a whole one, staged in its Q tile; then the stage
+        // is free
+        sy.wait(kReadyY, (i - 1) & 1);
+        const int t = static_cast<int>(t0) + (i - 1) * C, a = (i - 1) % 3;
+        const unsigned char *y = sm + oKQ + a * kStageKQ + kHalf;
+        if (!*abort) {
+          tma_store_4d(&maps.y, y, p0, h, t, b);
+          if (p0 + 64 < P) tma_store_4d(&maps.y, y + 2 * kHalf, p0 + 64, h, t, b);
+        }
+        tma_store_wait_read();
+        mbar_arrive(bar + kEmptyKQ + a);
       }
       for (int i = nc > 2 ? nc - 2 : 0; i < nc; ++i) sy.drain(kFullV + (i & 1), (i / 2) & 1);
+      tma_store_wait_all();
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------- tensor-core issue
-    constexpr uint32_t idKK = idesc_bf16(128, 64, 0, 0);       // both K-major
-    constexpr uint32_t idTK = idesc_bf16(128, 64, 1, 0);       // A as stored by step
-    constexpr uint32_t idH = idesc_bf16(128, 16 * NK, 0, 1);  // B as stored by step
-    constexpr uint32_t kLo = kHalf >> 4;  // hi -> lo of T and P
     const uint32_t on = elect_one();
-    // slice k of a K-major tile whose 64-wide halves lie 2 kHalf apart
-    auto kslice = [](int k) { return static_cast<uint32_t>((k >> 2) * (2 * kHalf >> 4) + (k & 3) * 2); };
     // after a timeout nothing is issued any more (commits still complete)
     auto alive = [&]() { return !__any_sync(0xffffffffu, *abort); };
     auto ready = [&](int i, uint32_t parity) {
@@ -451,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (alive()) {
         const uint32_t d = desc_lo(sbase + oKQ + sst * kStageKQ, 16);
-#pragma unroll 4
-        for (int k = 0; k < NK; ++k) mma_ss(kColS, d + kslice(k), d + kslice(k), idKK, k > 0, on);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) mma_ss(kColS, d + kslice(k), d + kslice(k), kIdKK, k > 0, on);
       }
       mma_commit(bar + kDoneS + (ns & 1), on);
       ++ns;
@@ -463,24 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ns < nc && (ns == 0 || ready(kFreeS, (ns - 1) & 1)) && ready(kFullKQ + sst, (ns / 3) & 1))
         issue_scores();
     };
-    // y of chunk i, staged in the Q tile of its stage t, which is released
-    // once it has been read
-    auto store = [&](int i, int t) {
-      if (y_tma && (i + 1) * C <= total && on && !*abort) {
-        unsigned char *d = sm + oKQ + t * kStageKQ + kHalf;
-        const int step = static_cast<int>(t0) + i * C;
-        tma_store_4d(&maps.y, d, p0, h, step, b);
-        if (p0 + 64 < P) tma_store_4d(&maps.y, d + 2 * kHalf, p0 + 64, h, step, b);
-      }
-    };
-    auto release = [&](int t) {
-      if (on) {
-        tma_store_wait_read();
-        mbar_arrive(bar + kEmptyKQ + t);
-      }
-    };
     int st = 0;  // i % 3
-    for (int i = 0; i < nc; ++i) {
+    for (int i = 0; i < nc; ++i, st = st == 2 ? 0 : st + 1) {
       const uint32_t kq = sbase + oKQ + st * kStageKQ;
       while (ns <= i) {
         if (ns > 0) sy.wait(kFreeS, (ns - 1) & 1);
@@ -494,11 +487,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
           const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
-          mma_ts(kColX, hi, dK + kslice(k), idKK, k > 0, on);
-          mma_ts(kColX, hi + 16, dK + kslice(k), idKK, 1, on);
+          mma_ts(kColX, hi, dK + kslice(k), kIdKK, k > 0, on);
+          mma_ts(kColX, hi + 16, dK + kslice(k), kIdKK, 1, on);
         }
       }
       mma_commit(bar + kDoneX, on);
+      if (alive()) {  // O1 = H Q^T
+        const uint32_t dQ = desc_lo(kq + kHalf, 16), o1 = kColO1 + (i & 1) * 64;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
+          mma_ts(o1, hi, dQ + kslice(k), kIdKK, k > 0, on);
+          mma_ts(o1, hi + 16, dQ + kslice(k), kIdKK, 1, on);
+        }
+      }
+      mma_commit(bar + kDoneO1, on);
+      // T of this chunk may hang on the S of the next having been issued
+      for (uint32_t n = 0; ns < nc && n < 1000 && !ready(kReadyT + (i & 1), (i / 2) & 1); ++n)
+        try_scores();
       const uint32_t dT = desc_lo(sbase + oT + (i & 1) * 2 * kHalf, 16);
       sy.wait(kReadyT + (i & 1), (i / 2) & 1);
       sy.wait(kFullV + (i & 1), (i / 2) & 1);
@@ -506,38 +512,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (alive()) {  // U^T = V^T T^T
         const uint32_t dV = desc_lo(sbase + oV, kHalf);
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma_ss(kColU, dV + k * 128, dT + k * 2, idTK, k > 0, on);
-          mma_ss(kColU, dV + k * 128, dT + kLo + k * 2, idTK, 1, on);
+          mma_ss(kColU, dV + k * 128, dT + k * 2, kIdTK, k > 0, on);
+          mma_ss(kColU, dV + k * 128, dT + kLoTile + k * 2, kIdTK, 1, on);
         }
       }
       mma_commit(bar + kEmptyV, on);
-      if (i > 0) {
-        sy.wait(kFreeO, (i - 1) & 1);
-        tc_fence_after();
-        store(i - 1, st == 0 ? 2 : st - 1);
-      }
-      if (alive()) {  // O1 = H Q^T
-        const uint32_t dQ = desc_lo(kq + kHalf, 16);
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
-          mma_ts(kColO1, hi, dQ + kslice(k), idKK, k > 0, on);
-          mma_ts(kColO1, hi + 16, dQ + kslice(k), idKK, 1, on);
-        }
-      }
-      mma_commit(bar + kDoneO1, on);
-      try_scores();
-      if (i > 0) release(st == 0 ? 2 : st - 1);
       sy.wait(kReadyR, i & 1);
       tc_fence_after();
       if (alive()) {  // U^T += R^T T^T
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma_ts(kColU, kColX + 16 * k, dT + k * 2, idKK, 1, on);
-          mma_ts(kColU, kColX + 16 * k + 8, dT + k * 2, idKK, 1, on);
-          mma_ts(kColU, kColX + 16 * k, dT + kLo + k * 2, idKK, 1, on);
+          mma_ts(kColU, kColX + 16 * k, dT + k * 2, kIdKK, 1, on);
+          mma_ts(kColU, kColX + 16 * k + 8, dT + k * 2, kIdKK, 1, on);
+          mma_ts(kColU, kColX + 16 * k, dT + kLoTile + k * 2, kIdKK, 1, on);
         }
       }
       mma_commit(bar + kDoneU, on);
@@ -547,26 +536,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       if (alive()) {  // U'^T K
         const uint32_t dK = desc_lo(kq, 2 * kHalf);
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma_ts(kColH, kColUd + 16 * k, dK + k * 128, idH, k > 0, on);
-          mma_ts(kColH, kColUd + 16 * k + 8, dK + k * 128, idH, 1, on);
+          mma_ts(kColH, kColX + 16 * k, dK + k * 128, idH, k > 0, on);
+          mma_ts(kColH, kColX + 16 * k + 8, dK + k * 128, idH, 1, on);
         }
       }
       mma_commit(bar + kDoneH, on);
+      if (!y_tma) mma_commit(bar + kEmptyKQ + st, on);
+      if (i > 0) {
+        sy.wait(kFreeO, (i - 1) & 1);
+        tc_fence_after();
+      }
       if (alive()) {  // O2 = U^T (Q K^T o D)^T
         const uint32_t dP = desc_lo(sbase + oP + (i & 1) * 2 * kHalf, 16);
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
-          mma_ts(kColO2, kColU + 16 * k, dP + k * 2, idKK, k > 0, on);
-          mma_ts(kColO2, kColU + 16 * k + 8, dP + k * 2, idKK, 1, on);
-          mma_ts(kColO2, kColU + 16 * k, dP + kLo + k * 2, idKK, 1, on);
+          mma_ts(kColO2, kColU + 16 * k, dP + k * 2, kIdKK, k > 0, on);
+          mma_ts(kColO2, kColU + 16 * k + 8, dP + k * 2, kIdKK, 1, on);
+          mma_ts(kColO2, kColU + 16 * k, dP + kLoTile + k * 2, kIdKK, 1, on);
         }
       }
       mma_commit(bar + kDoneO, on);
       mma_commit(bar + kFreeP + (i & 1), on);
       try_scores();
-      st = st == 2 ? 0 : st + 1;
     }
     // every product done before the tensor memory is freed, and every commit
     // arrived, those too that nobody waits for: an arrival at the shared
@@ -574,10 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nc > 0) {
       sy.drain(kDoneO, (nc - 1) & 1);
       sy.drain(kEmptyV, (nc - 1) & 1);
+      for (int i = y_tma ? nc : (nc > 3 ? nc - 3 : 0); i < nc; ++i)
+        sy.drain(kEmptyKQ + i % 3, (i / 3) & 1);
       for (int i = nc > 2 ? nc - 2 : 0; i < nc; ++i) sy.drain(kFreeP + (i & 1), (i / 2) & 1);
-      sy.wait(kFreeO, (nc - 1) & 1);
-      store(nc - 1, st == 0 ? 2 : st - 1);
-      tma_store_wait_all();
     }
   } else if (warp == 2) {
     // --------------------------------------------------------- the gates
@@ -643,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = p0 + 32 * q + lane;
     const uint32_t tl = static_cast<uint32_t>(32 * q) << 16;
     const int64_t base = (sh * p.P + row) * p.N + 32 * e;
-    OutT *yp = static_cast<OutT *>(p.y) + b * p.sy[0] + h * p.sy[2] + (t0 + 16 * e) * p.sy[1] + row;
+    OutT *yp = static_cast<OutT *>(p.y) + b * p.sy[0] + h * p.sy[2] + t0 * p.sy[1] + row;
     float H[32];
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
@@ -682,9 +674,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto output = [&](int i) {
       sy.wait(kDoneO, i & 1);
       tc_fence_after();
-      const float *eo = reinterpret_cast<const float *>(sm + oDecay + (i % 3) * kDecay) + 2 * C + 16 * e;
+      const float *eo =
+          reinterpret_cast<const float *>(sm + oDecay + (i % 3) * kDecay) + 2 * C + 16 * e;
       float v[16], o[16];
-      tmem_get16x2(tl + kColO1 + 16 * e, tl + kColO2 + 16 * e, v, o);
+      tmem_get16x2(tl + kColO1 + (i & 1) * 64 + 16 * e, tl + kColO2 + 16 * e, v, o);
 #pragma unroll
       for (int j = 0; j < 16; j += 4) {
         const float4 x = *reinterpret_cast<const float4 *>(eo + j);
@@ -694,6 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         o[j + 3] = fmaf(x.w, v[j + 3], o[j + 3]);
       }
       tc_fence_before();
+      warp_arrive(bar + kFreeO, lane);
+      if (lane == 0) mbar_arrive(bar + kFreeD + i % 3);
       const int left = total - i * C - 16 * e;
       if (y_tma && (i + 1) * C <= total) {
         if constexpr (sizeof(OutT) == 2) {
@@ -703,14 +698,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<OutT *>(d + (ycol ^ ((j & 7) << 4)) + j * 128) = from_f32<OutT>(o[j]);
           fence_async_smem();
         }
+        warp_arrive(bar + kReadyY, lane);
       } else if (row < P) {
-        OutT *yr = yp + static_cast<int64_t>(i) * C * p.sy[1];
+        OutT *yr = yp + static_cast<int64_t>(i * C + 16 * e) * p.sy[1];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           if (j < left) yr[j * p.sy[1]] = from_f32<OutT>(o[j]);
       }
-      warp_arrive(bar + kFreeO, lane);
-      if (lane == 0) mbar_arrive(bar + kFreeD + i % 3);
     };
     for (int i = 0;; ++i) {
       if (i > 0) update(i - 1);
@@ -773,8 +767,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           split2(v[j] * d.x, v[j + 1] * d.y, hi[j / 2], lo[j / 2]);
           split2(v[j + 2] * d.z, v[j + 3] * d.w, hi[j / 2 + 1], lo[j / 2 + 1]);
         }
-        tmem_st8(tl + kColUd + 16 * e, hi);
-        tmem_st8(tl + kColUd + 16 * e + 8, lo);
+        tmem_st8(tl + kColX + 16 * e, hi);
+        tmem_st8(tl + kColX + 16 * e + 8, lo);
 #pragma unroll
         for (int j = 0; j < 8; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
         tmem_st8(tl + kColU + 16 * e, hi);
@@ -796,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // group gr takes the chunks of its parity
     const int q = warp & 3, gr = (warp - 20) >> 2, at = tid - 640 - gr * kAux, aw = at >> 5;
     const uint32_t tl = static_cast<uint32_t>(32 * q) << 16;
-    float *scr = reinterpret_cast<float *>(sm + oScr) + gr * 4 * kBlk;
+    float *scr = reinterpret_cast<float *>(sm + oScr) + gr * kScr;
     unsigned char *pt = sm + oP + gr * 2 * kHalf, *tt = sm + oT + gr * 2 * kHalf;
     const float *beta_s = reinterpret_cast<const float *>(sm + oGate + gr * kGate);
     const float *cum_s = beta_s + C;
@@ -884,11 +878,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         invert32(scr + (q ? bA22 : bA11) * kBlk, lane);
       }
       bar_sync(kBarAux + gr, kAux);
-      // T21 = -T22 (A21 T11), a 16 x 16 block of a warp
-      const int r0 = 16 * (aw >> 1), n0 = 16 * (aw & 1);
-      float z[2][4];
-      tiles<32>(scr + bA21 * kBlk + r0, 1, kLd, scr + bA11 * kBlk + n0, lane, z);
-      store_tiles(scr + bZ * kBlk + r0 * kLd + n0, lane, z, 1.f);
+      // T21 = -T22 (A21 T11)
+      const int r2 = 2 * (at >> 3), c4 = 4 * (at & 7);
+      float2 z[2][2];
+      prod_t<32>(scr + bA21 * kBlk + r2, scr + bA11 * kBlk + c4, z);
+      store24(scr + bZ * kBlk + r2 * kLd + c4, z, 1.f);
 #pragma unroll 1
       for (int w = 0; w < 2; ++w) {
         // pairs of T11 and T22, times b: 8 columns of a row
@@ -911,18 +905,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(tt + kHalf + o) = lo;
       }
       bar_sync(kBarAux + gr, kAux);
-      tiles<32>(scr + bA22 * kBlk + r0 * kLd, kLd, 1, scr + bZ * kBlk + n0, lane, z);
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        const int c = n0 + 8 * n + 2 * (lane & 3);
-        const float2 nb = *reinterpret_cast<const float2 *>(beta_s + c);
+      prod_n<32>(scr + bA22 * kBlk + r2 * kLd, scr + bZ * kBlk + c4, z);
+      {
+        const float4 nb = *reinterpret_cast<const float4 *>(beta_s + c4);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t hi, lo;
-          split2(-z[n][2 * k] * nb.x, -z[n][2 * k + 1] * nb.y, hi, lo);
-          const uint32_t o = swz(32 + r0 + 8 * k + (lane >> 2), c >> 3) + 4 * (lane & 3);
-          *reinterpret_cast<uint32_t *>(tt + o) = hi;
-          *reinterpret_cast<uint32_t *>(tt + kHalf + o) = lo;
+          uint2 hi, lo;
+          split2(-nb.x * z[k][0].x, -nb.y * z[k][0].y, hi.x, lo.x);
+          split2(-nb.z * z[k][1].x, -nb.w * z[k][1].y, hi.y, lo.y);
+          const uint32_t o = swz(32 + r2 + k, c4 >> 3) + 2 * (c4 & 4);
+          *reinterpret_cast<uint2 *>(tt + o) = hi;
+          *reinterpret_cast<uint2 *>(tt + kHalf + o) = lo;
         }
       }
       fence_async_smem();
@@ -955,10 +948,10 @@ bool map_strides(const int64_t (&s)[3], int64_t batch, int64_t L, int64_t heads)
   return true;
 }
 
-// box {64, 1, C, 1}, 128-byte swizzle; channels and steps past the end read
+// box {64, 1, steps, 1}, 128-byte swizzle; channels and steps past the end read
 // as zeros
 bool encode(CUtensorMap *m, const void *ptr, int64_t width, int64_t heads, int64_t L,
-            int64_t batch, const int64_t (&s)[3]) {
+            int64_t batch, const int64_t (&s)[3], cuuint32_t steps) {
   auto enc = encoder();
   if (!enc) return false;
   const auto st = [](int64_t n, int64_t stride) {
@@ -967,7 +960,7 @@ bool encode(CUtensorMap *m, const void *ptr, int64_t width, int64_t heads, int64
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads),
                         static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(batch)};
   cuuint64_t strides[3] = {st(heads, s[2]), st(L, s[1]), st(batch, s[0])};
-  cuuint32_t box[4] = {64, 1, C, 1}, estr[4] = {1, 1, 1, 1};
+  cuuint32_t box[4] = {64, 1, steps, 1}, estr[4] = {1, 1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -991,13 +984,13 @@ bool delta_chunk_applies(const DeltaParams &p, bool in_bf16) {
 
 cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t stream) {
   Maps maps;
-  if (!encode(&maps.q, p.q, p.N, p.G, p.L, p.batch, p.sq) ||
-      !encode(&maps.k, p.k, p.N, p.G, p.L, p.batch, p.sk) ||
-      !encode(&maps.v, p.v, p.P, p.H, p.L, p.batch, p.sv))
+  if (!encode(&maps.q, p.q, p.N, p.G, p.L, p.batch, p.sq, C) ||
+      !encode(&maps.k, p.k, p.N, p.G, p.L, p.batch, p.sk, C) ||
+      !encode(&maps.v, p.v, p.P, p.H, p.L, p.batch, p.sv, C))
     return cudaErrorInvalidValue;
   // y through tensor maps: bf16, rows on 16-byte boundaries
   const int y_tma = out_bf16 && al16(p.y) && map_strides(p.sy, p.batch, p.L, p.H) &&
-                    encode(&maps.y, p.y, p.P, p.H, p.L, p.batch, p.sy);
+                    encode(&maps.y, p.y, p.P, p.H, p.L, p.batch, p.sy, C);
   const unsigned grid = static_cast<unsigned>(p.seqs * p.H * ((p.P + 127) / 128));
   auto run = [&](auto kernel) {
     // per launch: the attribute belongs to the current device
