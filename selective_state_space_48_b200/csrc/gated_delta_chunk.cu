@@ -79,7 +79,7 @@ constexpr int kGate = 2 * C * 4;
 constexpr int oDecay = oGate + 2 * kGate;  // three of (2^(c_last - c), 2^c, scale 2^c) [C]
 constexpr int kDecay = 3 * C * 4;
 constexpr int oBar = oDecay + 3 * kDecay;
-constexpr int kBars = 34;
+constexpr int kBars = 35;
 constexpr int oTmemSlot = oBar + kBars * 8;
 constexpr int oAbort = oTmemSlot + 4;
 constexpr int kSmemBytes = oAbort + 4;
@@ -97,14 +97,14 @@ constexpr uint32_t kColS = 448;   // K K^T (lanes 0..63), Q K^T (64..127)
 constexpr uint32_t kTmemCols = 512;
 
 // Barriers.  Tiles landed and released; per chunk, products done (S, X, U, O1,
-// the update, O) and operands ready (H; R; U; T and P), S and O drained; y staged; the two P buffers released; the gates written (the decays have three buffers, the rest
+// the update, O) and operands ready (H; R; U'; U; T and P), S and O drained; y staged; the two P buffers released; the gates written (the decays have three buffers, the rest
 // two) and their two and three buffers released.  A waiter may not fall two
 // phases behind: where it could, the barriers are a ring.  The groups arrive
 // one lane per warp.
 constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 9, kDoneX = 11,
               kDoneU = 12, kDoneO1 = 13, kDoneH = 14, kDoneO = 15, kReadyH = 16, kReadyR = 17,
-              kReadyU = 18, kFreeO = 19, kReadyY = 20, kFreeS = 21, kReadyT = 22, kFreeP = 24,
-              kReadyG = 26, kFreeG = 29, kFreeD = 31;  // .. 33
+              kReadyU = 18, kReadyO = 19, kFreeO = 20, kReadyY = 21, kFreeS = 22, kReadyT = 23,
+              kFreeP = 25, kReadyG = 27, kFreeG = 30, kFreeD = 32;  // .. 34
 // arrivals that complete a barrier's phase
 __device__ __forceinline__ int bar_count(int i) {
   if (i == kFreeS || i == kReadyT || i == kReadyT + 1 || i == kFreeG || i == kFreeG + 1)
@@ -492,21 +492,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kDoneX, on);
-      if (alive()) {  // O1 = H Q^T
-        const uint32_t dQ = desc_lo(kq + kHalf, 16), o1 = kColO1 + (i & 1) * 64;
-#pragma unroll
-        for (int k = 0; k < NK; ++k) {
-          const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
-          mma_ts(o1, hi, dQ + kslice(k), kIdKK, k > 0, on);
-          mma_ts(o1, hi + 16, dQ + kslice(k), kIdKK, 1, on);
-        }
-      }
-      mma_commit(bar + kDoneO1, on);
       // T of this chunk may hang on the S of the next having been issued
-      for (uint32_t n = 0; ns < nc && n < 1000 && !ready(kReadyT + (i & 1), (i / 2) & 1); ++n)
+      for (uint32_t n = 0; !ready(kReadyT + (i & 1), (i / 2) & 1); ++n) {
+        if (ns == nc || n == 1000) {
+          sy.wait(kReadyT + (i & 1), (i / 2) & 1);
+          break;
+        }
         try_scores();
+      }
       const uint32_t dT = desc_lo(sbase + oT + (i & 1) * 2 * kHalf, 16);
-      sy.wait(kReadyT + (i & 1), (i / 2) & 1);
       sy.wait(kFullV + (i & 1), (i / 2) & 1);
       if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of the chunk before has been read
       tc_fence_after();
@@ -530,6 +524,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kDoneU, on);
+      if (alive()) {  // O1 = H Q^T
+        const uint32_t dQ = desc_lo(kq + kHalf, 16), o1 = kColO1 + (i & 1) * 64;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
+          mma_ts(o1, hi, dQ + kslice(k), kIdKK, k > 0, on);
+          mma_ts(o1, hi + 16, dQ + kslice(k), kIdKK, 1, on);
+        }
+      }
+      mma_commit(bar + kDoneO1, on);
       try_scores();
       sy.wait(kDoneO1, i & 1);  // the update overwrites the pairs of H
       sy.wait(kReadyU, i & 1);
@@ -544,10 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(bar + kDoneH, on);
       if (!y_tma) mma_commit(bar + kEmptyKQ + st, on);
-      if (i > 0) {
-        sy.wait(kFreeO, (i - 1) & 1);
-        tc_fence_after();
-      }
+      if (i > 0) sy.wait(kFreeO, (i - 1) & 1);
+      sy.wait(kReadyO, i & 1);
+      tc_fence_after();
       if (alive()) {  // O2 = U^T (Q K^T o D)^T
         const uint32_t dP = desc_lo(sbase + oP + (i & 1) * 2 * kHalf, 16);
 #pragma unroll
@@ -769,6 +772,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st8(tl + kColX + 16 * e, hi);
         tmem_st8(tl + kColX + 16 * e + 8, lo);
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar + kReadyU, lane);
+        // (the pairs that only the output needs)
 #pragma unroll
         for (int j = 0; j < 8; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
         tmem_st8(tl + kColU + 16 * e, hi);
@@ -776,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(bar + kReadyU, lane);
+      warp_arrive(bar + kReadyO, lane);
     }
     if (p.last && row < P) {
 #pragma unroll
