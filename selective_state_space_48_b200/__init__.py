@@ -21,7 +21,9 @@ Functions mirror the C entry points:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct as _struct
 import threading
 
 import torch
@@ -792,73 +794,128 @@ class _on_device:
     and the stream: the caller's, or that device's current one."""
 
     def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         self._guard = torch.cuda.device(device)
         self._device, self._stream = device, stream
 
     def __enter__(self):
         self._guard.__enter__()
-        stream = self._stream
-        if stream is None:
-            stream = torch.cuda.current_stream(self._device)
-        elif stream.device != self._device:
-            self._guard.__exit__(None, None, None)
-            raise ValueError(f"stream is on {stream.device}, the tensors on {self._device}")
-        return stream
+        return self._stream or torch.cuda.current_stream(self._device)
 
     def __exit__(self, *exc):
         self._guard.__exit__(*exc)
 
 
-def _set_strides(a, **tensors):
-    for name, (t, dims) in tensors.items():
-        dst = getattr(a, "stride_" + name)
-        for i in range(dims):
-            dst[i] = t.stride(i)
+# The calls below fill their argument structs with one struct.pack and look
+# tensors over with plain comparisons, since a decode step's kernel takes a few
+# microseconds and ctypes fields one each; whatever does not compare equal goes
+# through the checks that say what is wrong.
+
+_PACK = {ctypes.c_int64: "q", ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_void_p: "P",
+         ctypes.c_uint64: "Q", ctypes.c_size_t: "N"}
+
+
+def _packer(args_type):
+    """``struct.pack`` of an argument struct's fields in order (native
+    alignment, as in C)."""
+    fmt = "@"
+    for _, t in args_type._fields_:
+        n = getattr(t, "_length_", None)
+        fmt += _PACK[t] if n is None else f"{n}{_PACK[t._type_]}"
+    pad = ctypes.sizeof(args_type) - _struct.calcsize(fmt)
+    return _struct.Struct(fmt + (f"{pad}x" if pad else "")).pack
+
+
+_entries = {}
+
+
+def _entry(name):
+    """The library function `name`, taking packed arguments."""
+    fn = _entries.get(name)
+    if fn is None:
+        fn = load_library()[name]  # a handle of its own, apart from lib.<name>
+        fn.argtypes, fn.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
+        _entries[name] = fn
+    return fn
+
+
+def _enqueue(name, packed, device, stream):
+    if stream is None and torch.cuda.current_device() == device.index:
+        rc = _entry(name)(packed, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with _on_device(device, stream) as s:
+            rc = _entry(name)(packed, s.cuda_stream)
+    if rc != MSS_OK:
+        raise MssError(rc, name)
+
+
+def _alike(t, dtype, device, shape):
+    """A tensor of this dtype, device and shape whose rows are contiguous."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and t.shape == shape and (t.stride(-1) == 1 or shape[-1] == 1))
+
+
+def _dense(t, dtype, device, shape):
+    return t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+                         and t.shape == shape and t.is_contiguous())
+
+
+def _same(t, dtype, device, shape):
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and t.shape == shape)
+
+
+def _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y,
+                  last_state, cu_seqlens, plan, spin_timeout_ns):
+    """The values of ``mss_delta_args`` in order, after the checks."""
+    if not isinstance(v, torch.Tensor) or not isinstance(q, torch.Tensor):
+        raise TypeError("q and v must be CUDA tensors")
+    if v.dim() != 4 or q.dim() != 4:
+        raise ValueError("q, k and v must have the dimensions (batch, seqlen, heads, width)")
+    batch, L, H, P = values = v.shape
+    G, N = q.shape[2], q.shape[3]
+    ind, dev, f32, cu = q.dtype, q.device, torch.float32, 0
+    keys, heads, seqs = (batch, L, G, N), (batch, L, H), batch
+    if cu_seqlens is not None:
+        _check_views(dev, [("cu_seqlens", cu_seqlens, torch.int32, None, "dense")])
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+            raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+        if batch != 1:
+            raise ValueError("packed sequences need batch 1")
+        seqs, cu = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
+    states = (seqs, H, P, N)
+    if not (dev.type == "cuda" and _alike(q, ind, dev, keys) and _alike(k, ind, dev, keys)
+            and _alike(v, ind, dev, values) and (y is None or _alike(y, y.dtype, dev, values))
+            and _same(dt, ind, dev, heads) and _same(beta, ind, dev, heads)
+            and A is not None and _dense(A, f32, dev, (H,)) and _dense(dt_bias, f32, dev, (H,))
+            and _dense(h0, f32, dev, states) and _dense(last_state, f32, dev, states)):
+        _check_views(dev, [
+            ("q", q, ind, keys, "rows"), ("k", k, ind, keys, "rows"),
+            ("v", v, ind, values, "rows"), ("dt", dt, ind, heads, None),
+            ("beta", beta, ind, heads, None), ("A", A, f32, (H,), "dense"),
+            ("dt_bias", dt_bias, f32, (H,), "dense"), ("h0", h0, f32, states, "dense"),
+            ("last_state", last_state, f32, states, "dense"), ("y", y, None, values, "rows")])
+    return (
+        batch, L, H, P, G, N, _dtype_code(ind), MSS_F32 if y is None else _dtype_code(y.dtype),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), A.data_ptr(), beta.data_ptr(),
+        0 if dt_bias is None else dt_bias.data_ptr(), bool(dt_softplus), bool(beta_sigmoid),
+        N ** -0.5 if scale is None else float(scale), 0 if h0 is None else h0.data_ptr(),
+        0 if y is None else y.data_ptr(), 0 if last_state is None else last_state.data_ptr(),
+        *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *dt.stride(), *beta.stride(),
+        *((0, 0, 0) if y is None else y.stride()[:3]), cu, seqs if cu else 0, int(plan),
+        int(spin_timeout_ns))
+
+
+_pack_delta = _packer(DeltaArgs)
 
 
 def make_gated_delta_args(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True,
                           beta_sigmoid=True, scale=None, h0=None, y=None, last_state=None,
                           cu_seqlens=None, plan=MSS_DELTA_AUTO, spin_timeout_ns=0) -> DeltaArgs:
-    if not isinstance(v, torch.Tensor) or not isinstance(q, torch.Tensor):
-        raise TypeError("q and v must be CUDA tensors")
-    if v.dim() != 4 or q.dim() != 4:
-        raise ValueError("q, k and v must have the dimensions (batch, seqlen, heads, width)")
-    batch, L, H, P = v.shape
-    G, N = q.shape[2], q.shape[3]
-    ind, dev = q.dtype, q.device
-    seqs = batch
-    if cu_seqlens is not None:
-        _check_views(dev, [("cu_seqlens", cu_seqlens, torch.int32, None, "dense")])
-        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-            raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
-        if batch != 1:
-            raise ValueError("packed sequences need batch 1")
-        seqs = cu_seqlens.numel() - 1
-    f32 = torch.float32
-    _check_views(dev, [
-        ("q", q, ind, (batch, L, G, N), "rows"), ("k", k, ind, (batch, L, G, N), "rows"),
-        ("v", v, ind, (batch, L, H, P), "rows"), ("dt", dt, ind, (batch, L, H), None),
-        ("beta", beta, ind, (batch, L, H), None), ("A", A, f32, (H,), "dense"),
-        ("dt_bias", dt_bias, f32, (H,), "dense"), ("h0", h0, f32, (seqs, H, P, N), "dense"),
-        ("last_state", last_state, f32, (seqs, H, P, N), "dense"),
-        ("y", y, None, (batch, L, H, P), "rows")])
-    a = DeltaArgs()
-    a.batch, a.seqlen, a.nheads, a.headdim, a.ngroups, a.dstate = batch, L, H, P, G, N
-    a.in_dtype = _dtype_code(ind)
-    a.out_dtype = _dtype_code(y.dtype) if y is not None else MSS_F32
-    a.q, a.k, a.v, a.dt, a.A, a.beta = (_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(beta))
-    a.dt_bias = _ptr(dt_bias)
-    a.dt_softplus, a.beta_sigmoid = int(bool(dt_softplus)), int(bool(beta_sigmoid))
-    a.scale = N ** -0.5 if scale is None else float(scale)
-    a.h0, a.y, a.last_state = _ptr(h0), _ptr(y), _ptr(last_state)
-    _set_strides(a, q=(q, 3), k=(k, 3), v=(v, 3), dt=(dt, 3), beta=(beta, 3))
-    if y is not None:
-        _set_strides(a, y=(y, 3))
-    if cu_seqlens is not None:
-        a.cu_seqlens, a.num_seqs = cu_seqlens.data_ptr(), seqs
-    a.plan = int(plan)
-    a.spin_timeout_ns = int(spin_timeout_ns)
-    return a
+    return DeltaArgs.from_buffer_copy(_pack_delta(*_delta_values(
+        q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y, last_state,
+        cu_seqlens, plan, spin_timeout_ns)))
 
 
 def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_sigmoid=True,
@@ -886,17 +943,14 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
         seqs = v.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
         last_state = torch.empty((seqs, v.shape[2], v.shape[3], q.shape[-1]),
                                  dtype=torch.float32, device=v.device)
-    a = make_gated_delta_args(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale,
-                              h0, y, last_state, cu_seqlens, plan)
-    lib = load_library()
-    with _on_device(q.device, stream) as s:
-        rc = lib.gated_delta_fwd(ctypes.byref(a), _stream_handle(s))
+    _enqueue("gated_delta_fwd", _pack_delta(*_delta_values(
+        q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y, last_state,
+        cu_seqlens, plan, 0)), q.device, stream)
+    if check_status:
+        with _on_device(q.device, stream) as s:
+            rc = load_library().mss_gated_delta_status(_stream_handle(s))
         if rc != MSS_OK:
-            raise MssError(rc, "gated_delta_fwd")
-        if check_status:
-            rc = lib.mss_gated_delta_status(_stream_handle(s))
-            if rc != MSS_OK:
-                raise MssError(rc, "mss_gated_delta_status")
+            raise MssError(rc, "mss_gated_delta_status")
     return (y, last_state) if return_last_state else y
 
 
@@ -917,29 +971,33 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
         raise TypeError("state and q must be CUDA tensors")
     if state.dim() != 4 or q.dim() != 3:
         raise ValueError("state must be (batch, heads, headdim, dstate), q (batch, groups, dstate)")
-    batch, H, P, N = state.shape
+    batch, H, P, N = shape = state.shape
     G, ind, dev, f32 = q.shape[1], q.dtype, q.device, torch.float32
     if y is None:
         y = torch.empty((batch, H, P), dtype=out_dtype, device=state.device)
-    _check_views(dev, [
-        ("state", state, f32, None, "dense"), ("q", q, ind, (batch, G, N), "rows"),
-        ("k", k, ind, (batch, G, N), "rows"), ("v", v, ind, (batch, H, P), "rows"),
-        ("dt", dt, ind, (batch, H), None), ("beta", beta, ind, (batch, H), None),
-        ("A", A, f32, (H,), "dense"), ("dt_bias", dt_bias, f32, (H,), "dense"),
-        ("y", y, None, (batch, H, P), "rows")])
-    a = DeltaUpdateArgs()
-    a.batch, a.nheads, a.headdim, a.ngroups, a.dstate = batch, H, P, G, N
-    a.in_dtype, a.out_dtype = _dtype_code(ind), _dtype_code(y.dtype)
-    a.state, a.q, a.k, a.v = _ptr(state), _ptr(q), _ptr(k), _ptr(v)
-    a.dt, a.A, a.beta, a.dt_bias, a.y = _ptr(dt), _ptr(A), _ptr(beta), _ptr(dt_bias), _ptr(y)
-    a.dt_softplus, a.beta_sigmoid = int(bool(dt_softplus)), int(bool(beta_sigmoid))
-    a.scale = N ** -0.5 if scale is None else float(scale)
-    _set_strides(a, q=(q, 2), k=(k, 2), v=(v, 2), dt=(dt, 2), beta=(beta, 2), y=(y, 2))
-    with _on_device(dev, stream) as s:
-        rc = load_library().gated_delta_update(ctypes.byref(a), _stream_handle(s))
-    if rc != MSS_OK:
-        raise MssError(rc, "gated_delta_update")
+    keys, values, heads = (batch, G, N), (batch, H, P), (batch, H)
+    if not (dev.type == "cuda" and _alike(q, ind, dev, keys) and _alike(k, ind, dev, keys)
+            and _alike(v, ind, dev, values) and _alike(y, y.dtype, dev, values)
+            and _same(dt, ind, dev, heads) and _same(beta, ind, dev, heads)
+            and _dense(state, f32, dev, shape) and A is not None and _dense(A, f32, dev, (H,))
+            and _dense(dt_bias, f32, dev, (H,))):
+        _check_views(dev, [
+            ("state", state, f32, None, "dense"), ("q", q, ind, keys, "rows"),
+            ("k", k, ind, keys, "rows"), ("v", v, ind, values, "rows"),
+            ("dt", dt, ind, heads, None), ("beta", beta, ind, heads, None),
+            ("A", A, f32, (H,), "dense"), ("dt_bias", dt_bias, f32, (H,), "dense"),
+            ("y", y, None, values, "rows")])
+    packed = _pack_update(
+        batch, H, P, G, N, _dtype_code(ind), _dtype_code(y.dtype), state.data_ptr(),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), A.data_ptr(), beta.data_ptr(),
+        0 if dt_bias is None else dt_bias.data_ptr(), bool(dt_softplus), bool(beta_sigmoid),
+        N ** -0.5 if scale is None else float(scale), y.data_ptr(), *q.stride()[:2], *k.stride()[:2],
+        *v.stride()[:2], *dt.stride(), *beta.stride(), *y.stride()[:2])
+    _enqueue("gated_delta_update", packed, dev, stream)
     return y
+
+
+_pack_update = _packer(DeltaUpdateArgs)
 
 
 # ------------------------------------------- norms before and after a block
@@ -963,36 +1021,53 @@ def _rows_of(name, t):
     return rows, (t.shape[-1] if stride is None else stride)
 
 
-def _norm_rows(a, device, shape, named):
-    """Pointers and row strides of the (..., width) tensors of a norm call."""
-    _check_views(device, [(n, t, d, shape, "rows") for n, t, d in named])
-    for name, t, _ in named:
-        if t is not None:
-            setattr(a, name, t.data_ptr())
-            setattr(a, "stride_" + name, _rows_of(name, t)[1])
+def _norm_rows(device, shape, named):
+    """[pointer, ...] and [row stride, ...] of the (..., width) tensors of a
+    norm call (0 for None)."""
+    ptrs, strides = [], []
+    for name, t, dtype in named:
+        if t is None:
+            ptrs.append(0)
+            strides.append(0)
+            continue
+        if not (_same(t, dtype, device, shape) and device.type == "cuda"):
+            _check_views(device, [(name, t, dtype, shape, "rows")])
+        ptrs.append(t.data_ptr())
+        strides.append(shape[-1] if t.is_contiguous() else _rows_of(name, t)[1])
+    return ptrs, strides
 
 
-def _norm_call(name, a, size_fn, device, stream):
-    """Runs one norm entry point, with the workspace it asks for."""
-    lib = load_library()
-    with _on_device(device, stream) as s:
-        ws = None
-        if size_fn is not None:
-            n = ctypes.c_size_t(0)
-            rc = getattr(lib, size_fn)(ctypes.byref(a), ctypes.byref(n))
-            if rc != MSS_OK:
-                raise MssError(rc, size_fn)
-            ws = alloc_workspace(int(n.value), device)
-            if ws is not None:
-                a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-        rc = getattr(lib, name)(ctypes.byref(a), _stream_handle(s))
-        if rc != MSS_OK:
-            raise MssError(rc, name)
-        if ws is not None:  # keep the workspace until the stream has used it
-            ws.record_stream(s)
+@functools.lru_cache(maxsize=1024)
+def _norm_workspace_bytes(name, rows, width, group, sums, device_index):
+    """Workspace bytes of a norm's backward of these sizes on this device."""
+    a = GatedNormArgs() if name == "gated" else AddNormArgs()
+    a.rows, a.width = rows, width
+    if name == "gated":
+        a.group_size, a.dweight = group, 1 if sums else None
+    else:
+        a.dweight, a.dscale = (1 if sums & 1 else None), (1 if sums & 2 else None)
+    fn = f"mss_{name}_rmsnorm_bwd_workspace_size"
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(device_index):
+        rc = getattr(load_library(), fn)(ctypes.byref(a), ctypes.byref(n))
+    if rc != MSS_OK:
+        raise MssError(rc, fn)
+    return int(n.value)
 
 
-def _gated_norm_args(x, z, weight, eps, group_size, norm_before_gate):
+def _norm_workspace(nbytes, device, stream):
+    """The workspace of a backward call; on the caller's own stream it is kept
+    until that stream has used it (on the current one the allocator does)."""
+    if not nbytes:
+        return None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws, ws.data_ptr()
+
+
+def _gated_norm_sizes(x, weight, group_size):
+    """rows, width, group size, and whether the groups share the weight."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
         raise TypeError("x must be a CUDA tensor with at least one dimension")
     width = x.shape[-1]
@@ -1000,16 +1075,15 @@ def _gated_norm_args(x, z, weight, eps, group_size, norm_before_gate):
     if gs < 1 or width % gs:
         raise ValueError(f"group_size {gs} must divide the width {width}")
     if not isinstance(weight, torch.Tensor) or weight.dim() != 1 or \
-            weight.numel() not in (width, gs):
+            weight.shape[0] not in (width, gs):
         raise ValueError(f"weight must have {width} or {gs} entries")
-    _check_views(x.device, [("weight", weight, torch.float32, None, "dense")])
-    a = GatedNormArgs()
-    a.rows, a.width, a.group_size = _rows_of("x", x)[0], width, gs
-    a.dtype = _dtype_code(x.dtype)
-    a.norm_before_gate = int(bool(norm_before_gate))
-    a.shared_weight = int(weight.numel() == gs)
-    a.eps, a.weight = float(eps), weight.data_ptr()
-    return a
+    if not _dense(weight, torch.float32, x.device, weight.shape):
+        _check_views(x.device, [("weight", weight, torch.float32, None, "dense")])
+    return x.numel() // max(width, 1), width, gs, weight.shape[0] == gs
+
+
+_pack_gated_norm = _packer(GatedNormArgs)
+_pack_add_norm = _packer(AddNormArgs)
 
 
 def gated_rmsnorm_fwd(x, z, weight, eps=1e-5, group_size=None, norm_before_gate=False, y=None,
@@ -1022,11 +1096,15 @@ def gated_rmsnorm_fwd(x, z, weight, eps=1e-5, group_size=None, norm_before_gate=
     ``group_size`` channels (default: the width), of x o silu(z), or of x
     with the gate applied after it (``norm_before_gate``).  Returns y like x.
     """
-    a = _gated_norm_args(x, z, weight, eps, group_size, norm_before_gate)
+    rows, width, gs, shared = _gated_norm_sizes(x, weight, group_size)
+    dev, kind, shape = x.device, x.dtype, x.shape
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _norm_rows(a, x.device, x.shape, [("x", x, x.dtype), ("z", z, x.dtype), ("y", y, x.dtype)])
-    _norm_call("gated_rmsnorm_fwd", a, None, x.device, stream)
+        y = torch.empty(shape, dtype=kind, device=dev)
+    (px, pz, py), (sx, sz, sy) = _norm_rows(dev, shape, (("x", x, kind), ("z", z, kind),
+                                                         ("y", y, kind)))
+    _enqueue("gated_rmsnorm_fwd", _pack_gated_norm(
+        rows, width, gs, _dtype_code(kind), bool(norm_before_gate), shared, eps, px, pz,
+        weight.data_ptr(), py, 0, 0, 0, 0, sx, sz, sy, 0, 0, 0, 0, 0), dev, stream)
     return y
 
 
@@ -1035,26 +1113,32 @@ def gated_rmsnorm_bwd(x, z, weight, dy, eps=1e-5, group_size=None, norm_before_g
     """Gradients of sum(dy * y) for ``gated_rmsnorm_fwd`` on the same inputs.
     Returns a dict of dx, dz (x's dtype) and dweight (float32, like weight,
     None unless ``need_dweight``)."""
-    a = _gated_norm_args(x, z, weight, eps, group_size, norm_before_gate)
-    dx, dz = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    rows, width, gs, shared = _gated_norm_sizes(x, weight, group_size)
+    dev, kind, shape = x.device, x.dtype, x.shape
+    dx, dz = (torch.empty(shape, dtype=kind, device=dev) for _ in range(2))
     dw = torch.empty_like(weight) if need_dweight else None
-    _norm_rows(a, x.device, x.shape, [("x", x, x.dtype), ("z", z, x.dtype), ("dy", dy, x.dtype),
-                                      ("dx", dx, x.dtype), ("dz", dz, x.dtype)])
-    a.dweight = _ptr(dw)
-    _norm_call("gated_rmsnorm_bwd", a, "mss_gated_rmsnorm_bwd_workspace_size", x.device, stream)
+    (px, pz, pdy, pdx, pdz), (sx, sz, sdy, sdx, sdz) = _norm_rows(dev, shape, (
+        ("x", x, kind), ("z", z, kind), ("dy", dy, kind), ("dx", dx, kind), ("dz", dz, kind)))
+    nbytes = _norm_workspace_bytes("gated", rows, width, gs, 1, dev.index) if need_dweight else 0
+    ws, pws = _norm_workspace(nbytes, dev, stream)
+    _enqueue("gated_rmsnorm_bwd", _pack_gated_norm(
+        rows, width, gs, _dtype_code(kind), bool(norm_before_gate), shared, eps, px, pz,
+        weight.data_ptr(), 0, pdy, pdx, pdz, dw.data_ptr() if need_dweight else 0, sx, sz, 0, sdy,
+        sdx, sdz, pws, nbytes), dev, stream)
     return {"dx": dx, "dz": dz, "dweight": dw}
 
 
-def _add_norm_args(like, weight, scale, eps):
+def _add_norm_sizes(like, weight, scale):
     if not isinstance(like, torch.Tensor) or like.dim() < 1:
         raise TypeError("x and the residual must be CUDA tensors with at least one dimension")
-    width = like.shape[-1]
-    _check_views(like.device, [("weight", weight, torch.float32, (width,), "dense"),
-                               ("scale", scale, torch.float32, (width,), "dense")])
-    a = AddNormArgs()
-    a.rows, a.width = _rows_of("x", like)[0], width
-    a.eps, a.weight, a.scale = float(eps), weight.data_ptr(), _ptr(scale)
-    return a
+    width, dev, f32 = like.shape[-1], like.device, torch.float32
+    if weight is None or not _dense(weight, f32, dev, (width,)) or \
+            not _dense(scale, f32, dev, (width,)):
+        if not isinstance(weight, torch.Tensor):
+            raise TypeError("weight must be a CUDA tensor")
+        _check_views(dev, [("weight", weight, f32, (width,), "dense"),
+                           ("scale", scale, f32, (width,), "dense")])
+    return like.numel() // max(width, 1), width
 
 
 def add_rmsnorm_fwd(x, residual, weight, scale=None, eps=1e-5, residual_dtype=None, y=None,
@@ -1068,18 +1152,21 @@ def add_rmsnorm_fwd(x, residual, weight, scale=None, eps=1e-5, residual_dtype=No
     (width,) float32.  ``residual_out`` may be the residual itself.  Returns
     (y in x's dtype, r in the residual's dtype).
     """
-    a = _add_norm_args(x, weight, scale, eps)
+    rows, width = _add_norm_sizes(x, weight, scale)
+    dev, kind, shape = x.device, x.dtype, x.shape
     if residual_out is None:
         rd = residual.dtype if residual is not None else residual_dtype or torch.float32
-        residual_out = torch.empty(x.shape, dtype=rd, device=x.device)
+        residual_out = torch.empty(shape, dtype=rd, device=dev)
     rd = residual_out.dtype
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    a.dtype, a.res_dtype = _dtype_code(x.dtype), _dtype_code(rd)
-    _norm_rows(a, x.device, x.shape, [
-        ("x", x, x.dtype), ("residual", residual, rd), ("y", y, x.dtype),
-        ("residual_out", residual_out, rd)])
-    _norm_call("add_rmsnorm_fwd", a, None, x.device, stream)
+        y = torch.empty(shape, dtype=kind, device=dev)
+    (px, pr, py, po), (sx, sr, sy, so) = _norm_rows(dev, shape, (
+        ("x", x, kind), ("residual", residual, rd), ("y", y, kind),
+        ("residual_out", residual_out, rd)))
+    _enqueue("add_rmsnorm_fwd", _pack_add_norm(
+        rows, width, _dtype_code(kind), _dtype_code(rd), eps, px, pr,
+        0 if scale is None else scale.data_ptr(), weight.data_ptr(), py, po, 0, 0, 0, 0, 0, 0,
+        sx, sr, sy, so, 0, 0, 0, 0, 0, 0), dev, stream)
     return y, residual_out
 
 
@@ -1090,22 +1177,28 @@ def add_rmsnorm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, scale=
     dscale only.  Returns a dict of dx (dy's dtype), dresidual (the
     residual's dtype), dweight and dscale (float32; None where not asked for
     or there is no scale)."""
-    a = _add_norm_args(residual_out, weight, scale, eps)
+    rows, width = _add_norm_sizes(residual_out, weight, scale)
     if not isinstance(dy, torch.Tensor):
         raise TypeError("dy must be a CUDA tensor")
-    rd, td, shape, dev = residual_out.dtype, dy.dtype, residual_out.shape, residual_out.device
-    if scale is not None and need_dscale and x is None:
+    rd, kind, shape, dev = residual_out.dtype, dy.dtype, residual_out.shape, residual_out.device
+    need_dscale = need_dscale and scale is not None
+    if need_dscale and x is None:
         raise ValueError("dscale needs x")
-    dx = torch.empty(shape, dtype=td, device=dev)
+    dx = torch.empty(shape, dtype=kind, device=dev)
     dres = torch.empty(shape, dtype=rd, device=dev)
     dw = torch.empty_like(weight) if need_dweight else None
-    ds = torch.empty_like(scale) if scale is not None and need_dscale else None
-    a.dtype, a.res_dtype = _dtype_code(td), _dtype_code(rd)
-    _norm_rows(a, dev, shape, [
-        ("residual_out", residual_out, rd), ("dy", dy, td), ("dresidual_out", dresidual_out, rd),
-        ("x", x if ds is not None else None, td), ("dx", dx, td), ("dresidual", dres, rd)])
-    a.dweight, a.dscale = _ptr(dw), _ptr(ds)
-    _norm_call("add_rmsnorm_bwd", a, "mss_add_rmsnorm_bwd_workspace_size", dev, stream)
+    ds = torch.empty_like(scale) if need_dscale else None
+    (po, pdy, pdo, px, pdx, pdr), (so, sdy, sdo, sx, sdx, sdr) = _norm_rows(dev, shape, (
+        ("residual_out", residual_out, rd), ("dy", dy, kind), ("dresidual_out", dresidual_out, rd),
+        ("x", x if need_dscale else None, kind), ("dx", dx, kind), ("dresidual", dres, rd)))
+    sums = (1 if need_dweight else 0) + (2 if need_dscale else 0)
+    nbytes = _norm_workspace_bytes("add", rows, width, 0, sums, dev.index) if sums else 0
+    ws, pws = _norm_workspace(nbytes, dev, stream)
+    _enqueue("add_rmsnorm_bwd", _pack_add_norm(
+        rows, width, _dtype_code(kind), _dtype_code(rd), eps, px, 0,
+        0 if scale is None else scale.data_ptr(), weight.data_ptr(), 0, po, pdy, pdo, pdx, pdr,
+        dw.data_ptr() if need_dweight else 0, ds.data_ptr() if need_dscale else 0,
+        sx, 0, 0, so, sdy, sdo, sdx, sdr, pws, nbytes), dev, stream)
     return {"dx": dx, "dresidual": dres, "dweight": dw, "dscale": ds}
 
 
