@@ -841,7 +841,7 @@ def _entry(name):
 
 
 def _enqueue(name, packed, device, stream):
-    if stream is None and torch.cuda.current_device() == device.index:
+    if stream is None and torch._C._cuda_getDevice() == device.index:
         rc = _entry(name)(packed, torch._C._cuda_getCurrentRawStream(device.index))
     else:
         with _on_device(device, stream) as s:
@@ -859,6 +859,14 @@ def _alike(t, dtype, device, shape):
 def _dense(t, dtype, device, shape):
     return t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
                          and t.shape == shape and t.is_contiguous())
+
+
+def _new(like, dtype=None):
+    """An uninitialised contiguous tensor of the shape and device of `like`."""
+    if like.is_contiguous():  # (half the time of torch.empty)
+        return torch.empty_like(like) if dtype is None or dtype is like.dtype else \
+            torch.empty_like(like, dtype=dtype)
+    return torch.empty(like.shape, dtype=dtype or like.dtype, device=like.device)
 
 
 def _same(t, dtype, device, shape):
@@ -938,7 +946,7 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
     if not isinstance(v, torch.Tensor) or v.dim() != 4:
         raise ValueError("v must have the dimensions (batch, seqlen, heads, width)")
     if y is None:
-        y = torch.empty(v.shape, dtype=out_dtype, device=v.device)
+        y = _new(v, out_dtype)
     if return_last_state and last_state is None:
         seqs = v.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
         last_state = torch.empty((seqs, v.shape[2], v.shape[3], q.shape[-1]),
@@ -967,14 +975,14 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
     nheads, headdim, dstate) float32 is updated in place.  q, k: (batch,
     ngroups, dstate); v: (batch, nheads, headdim); dt, beta: (batch, nheads);
     views as for ``gated_delta_fwd``.  Returns y (batch, nheads, headdim)."""
-    if not isinstance(state, torch.Tensor) or not isinstance(q, torch.Tensor):
-        raise TypeError("state and q must be CUDA tensors")
+    if not all(isinstance(t, torch.Tensor) for t in (state, q, v)):
+        raise TypeError("state, q and v must be CUDA tensors")
     if state.dim() != 4 or q.dim() != 3:
         raise ValueError("state must be (batch, heads, headdim, dstate), q (batch, groups, dstate)")
     batch, H, P, N = shape = state.shape
     G, ind, dev, f32 = q.shape[1], q.dtype, q.device, torch.float32
     if y is None:
-        y = torch.empty((batch, H, P), dtype=out_dtype, device=state.device)
+        y = _new(v, out_dtype)
     keys, values, heads = (batch, G, N), (batch, H, P), (batch, H)
     if not (dev.type == "cuda" and _alike(q, ind, dev, keys) and _alike(k, ind, dev, keys)
             and _alike(v, ind, dev, values) and _alike(y, y.dtype, dev, values)
@@ -1099,7 +1107,7 @@ def gated_rmsnorm_fwd(x, z, weight, eps=1e-5, group_size=None, norm_before_gate=
     rows, width, gs, shared = _gated_norm_sizes(x, weight, group_size)
     dev, kind, shape = x.device, x.dtype, x.shape
     if y is None:
-        y = torch.empty(shape, dtype=kind, device=dev)
+        y = _new(x)
     (px, pz, py), (sx, sz, sy) = _norm_rows(dev, shape, (("x", x, kind), ("z", z, kind),
                                                          ("y", y, kind)))
     _enqueue("gated_rmsnorm_fwd", _pack_gated_norm(
@@ -1115,7 +1123,7 @@ def gated_rmsnorm_bwd(x, z, weight, dy, eps=1e-5, group_size=None, norm_before_g
     None unless ``need_dweight``)."""
     rows, width, gs, shared = _gated_norm_sizes(x, weight, group_size)
     dev, kind, shape = x.device, x.dtype, x.shape
-    dx, dz = (torch.empty(shape, dtype=kind, device=dev) for _ in range(2))
+    dx, dz = _new(x), _new(x)
     dw = torch.empty_like(weight) if need_dweight else None
     (px, pz, pdy, pdx, pdz), (sx, sz, sdy, sdx, sdz) = _norm_rows(dev, shape, (
         ("x", x, kind), ("z", z, kind), ("dy", dy, kind), ("dx", dx, kind), ("dz", dz, kind)))
@@ -1156,10 +1164,10 @@ def add_rmsnorm_fwd(x, residual, weight, scale=None, eps=1e-5, residual_dtype=No
     dev, kind, shape = x.device, x.dtype, x.shape
     if residual_out is None:
         rd = residual.dtype if residual is not None else residual_dtype or torch.float32
-        residual_out = torch.empty(shape, dtype=rd, device=dev)
+        residual_out = _new(x, rd)
     rd = residual_out.dtype
     if y is None:
-        y = torch.empty(shape, dtype=kind, device=dev)
+        y = _new(x)
     (px, pr, py, po), (sx, sr, sy, so) = _norm_rows(dev, shape, (
         ("x", x, kind), ("residual", residual, rd), ("y", y, kind),
         ("residual_out", residual_out, rd)))
@@ -1184,8 +1192,7 @@ def add_rmsnorm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, scale=
     need_dscale = need_dscale and scale is not None
     if need_dscale and x is None:
         raise ValueError("dscale needs x")
-    dx = torch.empty(shape, dtype=kind, device=dev)
-    dres = torch.empty(shape, dtype=rd, device=dev)
+    dx, dres = _new(residual_out, kind), _new(residual_out)
     dw = torch.empty_like(weight) if need_dweight else None
     ds = torch.empty_like(scale) if need_dscale else None
     (po, pdy, pdo, px, pdx, pdr), (so, sdy, sdo, sx, sdx, sdr) = _norm_rows(dev, shape, (

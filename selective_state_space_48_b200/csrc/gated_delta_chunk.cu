@@ -354,15 +354,6 @@ __device__ __forceinline__ constexpr uint32_t kslice(int k) {
   return static_cast<uint32_t>((k >> 2) * (2 * kHalf >> 4) + (k & 3) * 2);
 }
 
-// a tile on its way into L2
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *map, int c0, int c1, int c2,
-                                                int c3) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
-
 // NK: 16-wide slices of dstate (4 up to 64, else 8; TMA pads with zeros).
 // y_tma: whole chunks of y go out through their Q tile and a TMA store (bf16 rows that a tensor map takes): 16 two-byte
 // stores of a thread straight to memory took 1.3 us of a chunk's 4.5.
@@ -415,18 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < nc; ++i) {
         const int t = static_cast<int>(t0) + i * C;
         const int a = i % 3;
-        // the chunk after the next three is on its way into L2 by the time
-        // that its stage is free
-        if (i + 3 < nc) {
-          tma_prefetch_4d(&maps.k, 0, g, t + 3 * C, b);
-          tma_prefetch_4d(&maps.q, 0, g, t + 3 * C, b);
-          if (NK > 4) {
-            tma_prefetch_4d(&maps.k, 64, g, t + 3 * C, b);
-            tma_prefetch_4d(&maps.q, 64, g, t + 3 * C, b);
-          }
-          tma_prefetch_4d(&maps.v, p0, h, t + 3 * C, b);
-          if (p0 + 64 < P) tma_prefetch_4d(&maps.v, p0 + 64, h, t + 3 * C, b);
-        }
         if (i >= 3) sy.wait(kEmptyKQ + a, (i / 3 - 1) & 1);
         unsigned char *d = sm + oKQ + a * kStageKQ;
         mbar_expect_tx(bar + kFullKQ + a, kStageKQ);
@@ -534,7 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kEmptyV, on);
-      try_scores();
       sy.wait(kReadyR, i & 1);
       tc_fence_after();
       if (alive()) {  // U^T += R^T T^T
@@ -556,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kDoneO1, on);
+      try_scores();
       sy.wait(kDoneO1, i & 1);  // the update overwrites the pairs of H
       sy.wait(kReadyU, i & 1);
       tc_fence_after();
@@ -569,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(bar + kDoneH, on);
       if (!y_tma) mma_commit(bar + kEmptyKQ + st, on);
-      try_scores();
       if (i > 0) sy.wait(kFreeO, (i - 1) & 1);
       sy.wait(kReadyO, i & 1);
       tc_fence_after();

@@ -2,11 +2,11 @@
 // norm_bwd.cu): parameters, the mapping of a row onto threads, vector loads
 // and the sums over a row.
 //
-// A row is one (token, group) pair of gs channels.  TPR threads hold it in
+// A row is one (token, group) pair of gs channels.  Its threads hold it in
 // registers, NV pieces of 8 channels each, so every input is read once:
 // vectors of 8 neighbouring channels where sizes, strides and addresses
-// allow (VEC), else channels TPR apart, so that a warp's scalar accesses
-// still fall into whole sectors.
+// allow (VEC), else channels as far apart as there are threads, so that a
+// warp's scalar accesses still fall into whole sectors.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,22 +37,30 @@ struct Params {
   float *part, *part2;    // partial sums of dweight, dscale
 };
 
-// Threads of a row and pieces of a thread for a group of gs channels, and
-// the threads of a block: rows of up to 512 channels fit a warp or a part of
-// one (sums by shuffles alone), longer ones take a block.
+// How a row lies on threads.  Up to 512 channels: TPR threads of a warp or a
+// part of one, so that sums are shuffles alone, NV pieces each, several rows to
+// a block of 128.  Longer rows (TPR 0): a block per row, as many threads as it
+// takes at NV pieces each, at most 512 (2560 channels are 160 threads: with a
+// power of two the spare ones cost a third of the time).
 template <int TPR_, int NV_> struct Shape {
   static constexpr int TPR = TPR_, NV = NV_;
-  static constexpr int kThreads = TPR_ < 128 ? 128 : TPR_;
-  static constexpr int kRows = kThreads / TPR_;  // rows of a block side by side
+  static constexpr int kMaxThreads = TPR_ ? 128 : 512;
+  static constexpr int kRows = TPR_ ? 128 / (TPR_ ? TPR_ : 1) : 1;  // rows of a block
+  static int threads(int64_t gs) {
+    return TPR_ ? 128 : static_cast<int>(((gs + 8 * NV_ - 1) / (8 * NV_) + 31) / 32 * 32);
+  }
 };
-template <typename F> auto by_shape(int64_t gs, F f) {
+// Two pieces of a thread from 1024 channels on where rows move as vectors
+// (16384 rows of 4096 in bf16: forward 66 us, 82 with one piece, backward 140,
+// 157 with one), one where they are scalar (4096 rows of 1155: backward 33 us,
+// 38 with two).
+template <typename F> auto by_shape(int64_t gs, bool vec, F f) {
   if (gs <= 64) return f(Shape<8, 1>());
   if (gs <= 128) return f(Shape<16, 1>());
   if (gs <= 512) return f(Shape<32, 2>());
-  if (gs <= 2048) return f(Shape<128, 2>());
-  if (gs <= 4096) return f(Shape<256, 2>());
-  if (gs <= 8192) return f(Shape<512, 2>());
-  return f(Shape<512, 4>());
+  if (gs <= (vec ? 1024 : 4096)) return f(Shape<0, 1>());
+  if (gs <= 8192) return f(Shape<0, 2>());
+  return f(Shape<0, 4>());
 }
 
 // eight channels as they lie in memory
@@ -87,16 +95,29 @@ template <> struct Raw8<__nv_bfloat16> {
   }
 };
 
-template <int TPR, bool VEC> __device__ __forceinline__ int column(int i, int e, int lane) {
-  return VEC ? (i * TPR + lane) * 8 + e : i * TPR * 8 + e * TPR + lane;
-}
+// this thread's place in its row, the row's place in the block, and the
+// threads of a row
+template <typename S> struct Place {
+  int lane, sub, tpr;
+  __device__ __forceinline__ Place() {
+    tpr = S::TPR ? S::TPR : static_cast<int>(blockDim.x);
+    lane = S::TPR ? static_cast<int>(threadIdx.x) % (S::TPR ? S::TPR : 1)
+                  : static_cast<int>(threadIdx.x);
+    sub = S::TPR ? static_cast<int>(threadIdx.x) / (S::TPR ? S::TPR : 1) : 0;
+  }
+  // channel e of piece i
+  template <bool VEC> __device__ __forceinline__ int column(int i, int e) const {
+    return VEC ? (i * tpr + lane) * 8 + e : (i * 8 + e) * tpr + lane;
+  }
+};
 
 // piece i of a row of gs channels (zeros past its end)
-template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ Raw8<T> load8(const T *row, int i, int lane, int gs, bool valid) {
+template <bool VEC, typename T, typename S>
+__device__ __forceinline__ Raw8<T> load8(const T *row, int i, const Place<S> &at, int gs,
+                                         bool valid) {
   Raw8<T> r;
   if constexpr (VEC) {
-    const int c = column<TPR, true>(i, 0, lane);
+    const int c = at.template column<true>(i, 0);
     if (valid && c < gs) {
       r.load(row + c);
     } else {
@@ -106,7 +127,7 @@ __device__ __forceinline__ Raw8<T> load8(const T *row, int i, int lane, int gs, 
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = column<TPR, false>(i, e, lane);
+      const int c = at.template column<false>(i, e);
       r.set(e, valid && c < gs ? row[c] : from_f32<T>(0.f));
     }
   }
@@ -126,39 +147,39 @@ __device__ __forceinline__ void store_vec8(__nv_bfloat16 *p, const float (&v)[8]
   }
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <typename T, int TPR, bool VEC>
-__device__ __forceinline__ void store8(T *row, int i, int lane, int gs, const float (&v)[8]) {
+template <bool VEC, typename T, typename S>
+__device__ __forceinline__ void store8(T *row, int i, const Place<S> &at, int gs,
+                                       const float (&v)[8]) {
   if constexpr (VEC) {
-    const int c = column<TPR, true>(i, 0, lane);
+    const int c = at.template column<true>(i, 0);
     if (c < gs) store_vec8(row + c, v);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = column<TPR, false>(i, e, lane);
+      const int c = at.template column<false>(i, e);
       if (c < gs) row[c] = from_f32<T>(v[e]);
     }
   }
 }
 
-// Sums of NS values over the TPR threads of a row, given to all of them.
-// `sm` holds NS * 16 floats per call site in flight.
+// Sums of NS values over the threads of a row, given to all of them.  `sm`
+// holds 16 NS floats, another place each time in turn.
 template <int TPR, int NS>
 __device__ __forceinline__ void row_sum(float (&v)[NS], float *sm) {
 #pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+  for (int o = (TPR ? TPR : 32) / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int s = 0; s < NS; ++s) v[s] += __shfl_xor_sync(0xffffffffu, v[s], o);
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
+  if constexpr (TPR == 0) {
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
       for (int s = 0; s < NS; ++s) sm[s * 16 + (threadIdx.x >> 5)] = v[s];
     __syncthreads();
+    const int warps = static_cast<int>(blockDim.x) >> 5;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       float t = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) t += sm[s * 16 + w];
+      for (int w = 0; w < warps; ++w) t += sm[s * 16 + w];
       v[s] = t;
     }
   }

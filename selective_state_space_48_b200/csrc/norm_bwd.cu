@@ -7,11 +7,12 @@
 // so one pass over a row gives both sums it needs (a^2 and dn o a), taken
 // together, and its gradients; every input is read once and every gradient
 // written once, which bounds the kernel.  A block walks over rows of one
-// group, the next row's inputs loaded while the current one is summed, and
-// keeps its rows' sums for dweight (and dscale) in registers; they end in the
-// workspace as one line per warp or block, and a second launch adds the lines
-// in a fixed order.  There are about as many blocks as fit the SMs, so the
-// lines stay few beside the rows.
+// group, the next rows' inputs on their way into shared memory meanwhile (each
+// thread copies and reads places of its own, so nothing but the sums
+// synchronises), and keeps its rows' sums for dweight (and dscale) in
+// registers; they end in the workspace as one line per warp or block, and a
+// second launch adds the lines in a fixed order.  There are about as many
+// blocks as fit the SMs, so the lines stay few beside the rows.
 #include <algorithm>
 
 #include "norm.cuh"
@@ -22,147 +23,232 @@ namespace norm {
 namespace {
 
 // lines of partial sums that a block leaves
-template <typename S> constexpr int kLines = S::TPR < 32 ? 4 : S::kRows;
+template <typename S> constexpr int kLines = S::TPR ? 4 : 1;
+
+// 16-byte pieces of a thread's share of a row, and the rows on their way at a
+// time: about 100 KB of a block of 512 threads, so that two fit an SM
+template <typename T, typename R, int MODE, typename S> struct Ring {
+  static constexpr int kT = sizeof(T) / 2, kR = sizeof(R) / 2;  // of 8 channels
+  static constexpr int kPiece = 2 * kT + (MODE == kAdd ? 2 : 1) * kR;
+  static constexpr int kPieces = S::NV * kPiece;
+  static constexpr int kStages = kPieces <= 3 ? 4 : 2;
+  static constexpr bool kUsed = 16 * S::kMaxThreads * kPieces * kStages <= 200 * 1024;
+};
+
+__device__ __forceinline__ float rcp_mufu(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
 
 template <typename T, typename R, int MODE, typename S, bool VEC>
-__global__ void __launch_bounds__(S::kThreads) norm_bwd_kernel(const Params p) {
-  constexpr int TPR = S::TPR, NV = S::NV;
-  constexpr bool kAhead = VEC && NV <= 2;  // registers for the next row's inputs
+__global__ void __launch_bounds__(S::kMaxThreads,
+                                  S::TPR ? 4 : (S::NV == 1 && sizeof(T) == 2 ? 2 : 1))
+    norm_bwd_kernel(const Params p) {
+  constexpr int NV = S::NV;
+  using Rg = Ring<T, R, MODE, S>;
+  constexpr bool kRing = VEC && Rg::kUsed;
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float sm[2][32];
-  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const Place<S> at;
   const int c0 = static_cast<int>(blockIdx.y) * p.gs;
   const float *wr = p.weight + (p.shared ? 0 : c0);
   const int64_t step = static_cast<int64_t>(gridDim.x) * S::kRows;
 
-  Raw8<T> xn[NV], gn[NV];
-  Raw8<R> zn[NV], rn[MODE == kAdd ? NV : 1];
-  // add: the stored residual in zn, its upstream gradient in rn, x in xn only
-  // for dscale; gated: x in xn, z in zn
-  auto load = [&](int64_t row) {
-    const bool ok = row < p.rows;
-    const int64_t q = ok ? row : 0;
+  // add: the stored residual in zv, its upstream gradient in rv, x in xv only
+  // for dscale; gated: x in xv, z in zv
+  Raw8<T> xv[NV], gv[NV];
+  Raw8<R> zv[NV], rv[MODE == kAdd ? NV : 1];
+  const T *xp = static_cast<const T *>(p.x) + (MODE == kAdd ? 0 : c0);
+  const T *gp = static_cast<const T *>(p.dy) + c0;
+  const R *zp = MODE == kAdd ? static_cast<const R *>(p.res) : static_cast<const R *>(p.z) + c0;
+  const int64_t sz = MODE == kAdd ? p.sres : p.sz;
+  const bool has_x = MODE != kAdd || p.part2, has_r = MODE == kAdd && p.dres;
+  const uint32_t slot = smem_addr(ring), pitch = blockDim.x * 16;
+  // fp32 rows are copied so that neighbouring lanes of a row take neighbouring
+  // 16 bytes (a thread's own 32 would leave half of every sector to a second
+  // request): lane l of the W that share a row or a warp of it
+  constexpr int W = S::TPR ? S::TPR : 32;
+  const int l = threadIdx.x % W;
+  // row's inputs towards stage `st` (zeros behind the last row and channel)
+  auto fetch = [&](int64_t row, int st) {
+    if constexpr (kRing) {
+      uint32_t d = slot + st * Rg::kPieces * pitch;
+      const bool ok = row < p.rows;
+      const int64_t q = ok ? row : 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (MODE == kAdd) {
-        zn[i] = load8<R, TPR, VEC>(static_cast<const R *>(p.res) + q * p.sres, i, lane, p.gs, ok);
-        rn[i] = load8<R, TPR, VEC>(static_cast<const R *>(p.dres) + q * p.sdres, i, lane, p.gs,
-                                   ok && p.dres);
-        xn[i] = load8<T, TPR, VEC>(static_cast<const T *>(p.x) + q * p.sx, i, lane, p.gs,
-                                   ok && p.part2);
-      } else {
-        xn[i] = load8<T, TPR, VEC>(static_cast<const T *>(p.x) + q * p.sx + c0, i, lane, p.gs, ok);
-        zn[i] = load8<R, TPR, VEC>(static_cast<const R *>(p.z) + q * p.sz + c0, i, lane, p.gs, ok);
+      for (int i = 0; i < NV; ++i) {
+        const int c = at.template column<true>(i, 0);
+        auto put = [&](auto *base, bool on) {
+          if constexpr (sizeof(*base) == 2) {
+            const bool in = ok && c < p.gs && on;
+            copy16(d + threadIdx.x * 16, base + (in ? c : 0), in);
+            d += pitch;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int ck = c - 8 * l + 4 * (k * W + l);
+              const bool in = ok && ck < p.gs && on;
+              copy16(d + (threadIdx.x - l) * 32 + (k * W + l) * 16, base + (in ? ck : 0), in);
+            }
+            d += 2 * pitch;
+          }
+        };
+        put(has_x ? xp + q * p.sx : gp, has_x);
+        put(gp + q * p.sdy, true);
+        put(zp + q * sz, true);
+        if constexpr (MODE == kAdd)
+          put(has_r ? static_cast<const R *>(p.dres) + q * p.sdres : zp, has_r);
       }
-      gn[i] = load8<T, TPR, VEC>(static_cast<const T *>(p.dy) + q * p.sdy + c0, i, lane, p.gs, ok);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+  auto load = [&](int64_t row, int st) {
+    if constexpr (kRing) {
+      const unsigned char *d = ring + st * Rg::kPieces * pitch;
+      auto get = [&](auto &raw) {
+        constexpr int n = sizeof(raw) / 16;
+#pragma unroll
+        for (int k = 0; k < n; ++k)
+          reinterpret_cast<uint4 *>(&raw)[k] =
+              *reinterpret_cast<const uint4 *>(d + threadIdx.x * 16 * n + 16 * k);
+        d += n * pitch;
+      };
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        get(xv[i]);
+        get(gv[i]);
+        get(zv[i]);
+        if constexpr (MODE == kAdd) get(rv[i]);
+      }
+    } else {
+      const bool ok = row < p.rows;
+      const int64_t q = ok ? row : 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        xv[i] = load8<VEC>(xp + q * p.sx, i, at, p.gs, ok && has_x);
+        gv[i] = load8<VEC>(gp + q * p.sdy, i, at, p.gs, ok);
+        zv[i] = load8<VEC>(zp + q * sz, i, at, p.gs, ok);
+        if constexpr (MODE == kAdd)
+          rv[i] = load8<VEC>(static_cast<const R *>(p.dres) + q * p.sdres, i, at, p.gs, ok && has_r);
+      }
     }
   };
 
-  float w[NV][8], sc[MODE == kAdd ? NV : 1][8], dw[NV][8], ds[MODE == kAdd ? NV : 1][8];
+  float dw[NV][8], ds[MODE == kAdd ? NV : 1][8];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    load8<float, TPR, VEC>(wr, i, lane, p.gs, true).get(w[i]);
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
-    if constexpr (MODE == kAdd) {
+    for (int e = 0; e < 8; ++e) {
+      dw[i][e] = 0.f;
+      if constexpr (MODE == kAdd) ds[i][e] = 0.f;
+    }
+
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * S::kRows;
+  if constexpr (kRing) {
+#pragma unroll
+    for (int k = 0; k < Rg::kStages; ++k) fetch(first + at.sub + k * step, k);
+  }
+  int turn = 0, st = 0;
+  // the block's rows together: every thread of it takes part in the sums
+  for (int64_t base = first; base < p.rows; base += step, turn ^= 1) {
+    const int64_t row = base + at.sub;
+    const bool valid = row < p.rows;
+    if constexpr (kRing) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(Rg::kStages - 1) : "memory");
+      __syncwarp();  // the other lanes' copies
+    }
+    load(row, st);
+    float sg[MODE == kAdd ? 1 : NV][8], sum[2] = {0.f, 0.f};  // sg: sigmoid(z)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float a[8], d[8], w[8], z[8];
+      gv[i].get(d);
+      load8<VEC>(wr, i, at, p.gs, true).get(w);  // (from the L1: not worth its registers)
+      zv[i].get(z);
+      xv[i].get(a);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        ds[i][e] = 0.f;
-        sc[i][e] = 1.f;
+        if constexpr (MODE == kAdd) {
+          a[e] = z[e];
+        } else {
+          sg[i][e] = rcp_mufu(1.0f + ex2_mufu(-z[e] * kLog2e));
+          if (MODE == kGateAfter) a[e] *= z[e] * sg[i][e];
+          else d[e] *= z[e] * sg[i][e];
+        }
+        sum[0] = fmaf(a[e], a[e], sum[0]);
+        sum[1] = fmaf(d[e] * w[e], a[e], sum[1]);
       }
-      if (p.scale) load8<float, TPR, VEC>(p.scale, i, lane, p.gs, true).get(sc[i]);
+    }
+    row_sum<S::TPR, 2>(sum, sm[turn]);
+    // (0 behind the last row: with eps 0 its zeros would give NaN to dweight)
+    const float r = valid ? rsqrtf(fmaf(sum[0], p.inv, p.eps)) : 0.f;
+    // da = r dn - a r^2 mean(dn n) r, with n mean(dn n) = a r * r mean(dn a)
+    const float nm = -sum[1] * p.inv * r * r * r;
+    if constexpr (kRing) load(row, st);  // (again: not kept in registers)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float d[8], w[8], x[8], z[8], da[8], dz[8];
+      gv[i].get(d);
+      load8<VEC>(wr, i, at, p.gs, true).get(w);
+      zv[i].get(z);
+      xv[i].get(x);
+      if constexpr (MODE == kAdd) {
+        float up[8], sc[8];
+        rv[i].get(up);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float dr = d[e] * r;
+          dw[i][e] = fmaf(dr, z[e], dw[i][e]);
+          dz[e] = fmaf(z[e], nm, fmaf(dr, w[e], up[e]));
+          ds[i][e] = fmaf(dz[e], x[e], ds[i][e]);
+          da[e] = dz[e];
+        }
+        if (p.scale) {
+          load8<VEC>(p.scale, i, at, p.gs, true).get(sc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) da[e] *= sc[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float s = sg[i][e], g = z[e] * s, dr = d[e] * r;
+          const float dg = fmaf(s, z[e] - g, s);  // silu'(z) = s (1 + z - z s)
+          if constexpr (MODE == kGateAfter) {
+            const float a = x[e] * g;
+            dw[i][e] = fmaf(dr, a, dw[i][e]);
+            const float o = fmaf(a, nm, dr * w[e]);
+            dz[e] = o * x[e] * dg;
+            da[e] = o * g;
+          } else {
+            const float xr = dr * x[e], gw = g * w[e];
+            dw[i][e] = fmaf(xr, g, dw[i][e]);
+            dz[e] = xr * w[e] * dg;
+            da[e] = fmaf(x[e], nm, dr * gw);
+          }
+        }
+      }
+      if (valid) {
+        if (MODE != kAdd || p.dz)
+          store8<VEC>(static_cast<R *>(p.dz) + row * p.sdz + c0, i, at, p.gs, dz);
+        store8<VEC>(static_cast<T *>(p.dx) + row * p.sdx + c0, i, at, p.gs, da);
+      }
+    }
+    if constexpr (kRing) {
+      __syncwarp();  // read: the place may be written again
+      fetch(row + Rg::kStages * step, st);
+      st = st == Rg::kStages - 1 ? 0 : st + 1;
     }
   }
 
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * S::kRows;
-  if (kAhead) load(first + sub);
-  int turn = 0;
-  // the block's rows together: every thread of it takes part in the sums
-  for (int64_t base = first; base < p.rows; base += step, turn ^= 1) {
-    const int64_t row = base + sub;
-    const bool valid = row < p.rows;
-    if (!kAhead) load(row);
-    // a: the normed values; d: dy times the gate after the norm, if any
-    float a[NV][8], d[NV][8], sum[2] = {0.f, 0.f};
-    Raw8<T> xv[NV];
-    Raw8<R> zv[NV], rv[MODE == kAdd ? NV : 1];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      xv[i] = xn[i];
-      zv[i] = zn[i];
-      if constexpr (MODE == kAdd) rv[i] = rn[i];
-      gn[i].get(d[i]);
-      if constexpr (MODE == kAdd) {
-        zv[i].get(a[i]);
-      } else {
-        float z[8];
-        xv[i].get(a[i]);
-        zv[i].get(z);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float g = silu_f(z[e]);
-          if (MODE == kGateAfter) a[i][e] *= g;
-          else d[i][e] *= g;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum[0] = fmaf(a[i][e], a[i][e], sum[0]);
-        sum[1] = fmaf(d[i][e] * w[i][e], a[i][e], sum[1]);
-      }
-    }
-    Raw8<T> dyv[MODE == kGateBefore ? NV : 1];
-    if constexpr (MODE == kGateBefore) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) dyv[i] = gn[i];
-    }
-    if (kAhead) load(row + step);
-    row_sum<TPR, 2>(sum, sm[turn]);
-    const float r = rsqrtf(fmaf(sum[0], p.inv, p.eps));
-    const float m = sum[1] * r * r * p.inv;  // n mean(dn n) = a rstd * rstd mean(dn a)
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float da[8], dz[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = a[i][e] * r;
-        dw[i][e] = fmaf(d[i][e], n, dw[i][e]);
-        da[e] = r * fmaf(-a[i][e], m, d[i][e] * w[i][e]);
-      }
-      if constexpr (MODE == kAdd) {
-        float up[8], x[8];
-        rv[i].get(up);
-        xv[i].get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dz[e] = da[e] + up[e];
-          ds[i][e] = fmaf(dz[e], x[e], ds[i][e]);
-          da[e] = dz[e] * sc[i][e];
-        }
-        if (valid && p.dz)
-          store8<R, TPR, VEC>(static_cast<R *>(p.dz) + row * p.sdz, i, lane, p.gs, dz);
-      } else {
-        float z[8], x[8], g[8];
-        zv[i].get(z);
-        if constexpr (MODE == kGateBefore) dyv[i].get(g);
-        else xv[i].get(x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float s = __fdividef(1.0f, 1.0f + ex2_mufu(-z[e] * kLog2e));
-          const float dg = s * fmaf(z[e], 1.0f - s, 1.0f);
-          if (MODE == kGateBefore) {
-            dz[e] = g[e] * a[i][e] * r * w[i][e] * dg;
-          } else {
-            dz[e] = da[e] * x[e] * dg;
-            da[e] *= z[e] * s;
-          }
-        }
-        if (valid)
-          store8<R, TPR, VEC>(static_cast<R *>(p.dz) + row * p.sdz + c0, i, lane, p.gs, dz);
-      }
-      if (valid)
-        store8<T, TPR, VEC>(static_cast<T *>(p.dx) + row * p.sdx + c0, i, lane, p.gs, da);
-    }
-  }
+  // (no copy may land in the memory of a block that has ended)
+  if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory");
 
   // this block's lines of the sums over rows
   auto lines = [&](float *part, float (&v)[NV][8]) {
@@ -170,17 +256,17 @@ __global__ void __launch_bounds__(S::kThreads) norm_bwd_kernel(const Params p) {
     const int64_t width = static_cast<int64_t>(p.ng) * p.gs;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if constexpr (TPR < 32) {
+      if constexpr (S::TPR != 0) {  // rows of a warp
 #pragma unroll
-        for (int o = TPR; o < 32; o <<= 1)
+        for (int o = S::TPR; o < 32; o <<= 1)
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[i][e] += __shfl_xor_sync(0xffffffffu, v[i][e], o);
       }
-      if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
-        const int line = TPR < 32 ? static_cast<int>(threadIdx.x >> 5) : sub;
+      if (S::TPR == 0 || (threadIdx.x & 31) < S::TPR) {
+        const int line = S::TPR ? static_cast<int>(threadIdx.x >> 5) : 0;
         float *dst = part + (static_cast<int64_t>(blockIdx.x) * kLines<S> + line) * width + c0;
         // (the workspace is 16-byte aligned; a vector path has gs % 8 == 0)
-        store8<float, TPR, VEC>(dst, i, lane, p.gs, v[i]);
+        store8<VEC>(dst, i, at, p.gs, v[i]);
       }
     }
   };
@@ -212,9 +298,15 @@ __global__ void __launch_bounds__(512) line_sum_kernel(const float *pa, float *o
   }
 }
 
-// Row blocks of a backward call: about 1024 threads of every SM in all.
-template <typename S> int64_t row_blocks(int64_t rows, int64_t ng, int sms) {
-  const int64_t want = std::max<int64_t>(1, sms * (1024 / S::kThreads) / ng);
+// Row blocks of a backward call: as many in all as fit the SMs at once, by
+// their threads and their shared memory (of blocks of 128 threads with several
+// rows, 6 were best of 4 .. 16; rows that are not vectors leave longer lines of
+// scalars: 512 threads of an SM took 27 us for 4096 rows of 1155, 1024 took 33).
+template <typename S>
+int64_t row_blocks(int64_t rows, int64_t ng, int64_t gs, bool vec, int ring, int sms) {
+  int per = S::TPR ? 6 : std::min(8, (vec ? 1024 : 512) / S::threads(gs));
+  per = std::max(1, std::min(per, ring > 0 ? 220 * 1024 / (ring + 1024) : per));
+  const int64_t want = std::max<int64_t>(1, sms * per / ng);
   return std::min<int64_t>(want, (rows + S::kRows - 1) / S::kRows);
 }
 
@@ -226,24 +318,31 @@ mss_status sm_count(int *sms) {
   return MSS_OK;
 }
 
-// floats of one set of partial sums
+// floats that one set of partial sums takes at most (rows of scalars have no
+// more blocks than vectors of the same length)
 int64_t part_floats(int64_t rows, int64_t ng, int64_t gs, int sms) {
-  return by_shape(gs, [&](auto s) {
+  return by_shape(gs, true, [&](auto s) {
     using S = decltype(s);
-    return row_blocks<S>(rows, ng, sms) * kLines<S> * ng * gs;
+    return row_blocks<S>(rows, ng, gs, true, 0, sms) * kLines<S> * ng * gs;
   });
 }
 
 template <typename T, typename R, int MODE>
 cudaError_t launch(const Params &p, bool vec, int sms, float *dw, float *ds, cudaStream_t stream) {
-  return by_shape(p.gs, [&](auto shape) {
+  return by_shape(p.gs, vec, [&](auto shape) {
     using S = decltype(shape);
-    const int64_t rb = row_blocks<S>(p.rows, p.ng, sms);
+    const int threads = S::threads(p.gs);
+    using Rg = Ring<T, R, MODE, S>;
+    const int smem = vec && Rg::kUsed ? threads * 16 * Rg::kPieces * Rg::kStages : 0;
+    const int64_t rb = row_blocks<S>(p.rows, p.ng, p.gs, vec, smem, sms);
     const dim3 grid(static_cast<unsigned>(rb), static_cast<unsigned>(p.ng));
-    if (vec)
-      norm_bwd_kernel<T, R, MODE, S, true><<<grid, S::kThreads, 0, stream>>>(p);
-    else
-      norm_bwd_kernel<T, R, MODE, S, false><<<grid, S::kThreads, 0, stream>>>(p);
+    auto kernel = vec ? norm_bwd_kernel<T, R, MODE, S, true> : norm_bwd_kernel<T, R, MODE, S, false>;
+    if (smem > 40 * 1024) {  // (48 KB with the static part) per launch: the current device's
+      const cudaError_t a =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (a != cudaSuccess) return a;
+    }
+    kernel<<<grid, threads, smem, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!dw && !ds)) return e;
     // with a shared weight the groups of a line are lines of their own

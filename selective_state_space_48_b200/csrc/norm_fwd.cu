@@ -13,11 +13,11 @@ namespace norm {
 namespace {
 
 template <typename T, typename R, int MODE, typename S, bool VEC>
-__global__ void __launch_bounds__(S::kThreads) norm_fwd_kernel(const Params p) {
-  constexpr int TPR = S::TPR, NV = S::NV;
+__global__ void __launch_bounds__(S::kMaxThreads) norm_fwd_kernel(const Params p) {
+  constexpr int NV = S::NV;
   __shared__ float sm[16];
-  const int lane = threadIdx.x % TPR;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * S::kRows + threadIdx.x / TPR;
+  const Place<S> at;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * S::kRows + at.sub;
   const bool valid = unit < p.rows * p.ng;  // every thread takes part in the shuffles
   const int64_t row = valid ? unit / p.ng : 0;
   const int c0 = valid ? static_cast<int>(unit - row * p.ng) * p.gs : 0;
@@ -29,8 +29,8 @@ __global__ void __launch_bounds__(S::kThreads) norm_fwd_kernel(const Params p) {
   Raw8<R> zv[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    xv[i] = load8<T, TPR, VEC>(xr, i, lane, p.gs, valid);
-    zv[i] = load8<R, TPR, VEC>(zr, i, lane, p.gs, valid && zr);
+    xv[i] = load8<VEC>(xr, i, at, p.gs, valid);
+    zv[i] = load8<VEC>(zr, i, at, p.gs, valid && zr);
   }
   float a[NV][8], gate[NV][8], ss[1] = {0.f};
 #pragma unroll
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(S::kThreads) norm_fwd_kernel(const Params p) {
     if constexpr (MODE == kAdd) {
       if (p.scale) {
         float sc[8];
-        load8<float, TPR, VEC>(p.scale, i, lane, p.gs, true).get(sc);
+        load8<VEC>(p.scale, i, at, p.gs, true).get(sc);
 #pragma unroll
         for (int e = 0; e < 8; ++e) a[i][e] *= sc[e];
       }
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(S::kThreads) norm_fwd_kernel(const Params p) {
       // backward and the next block read
 #pragma unroll
       for (int e = 0; e < 8; ++e) a[i][e] = to_f32<R>(from_f32<R>(a[i][e] + z[e]));
-      if (valid) store8<R, TPR, VEC>(static_cast<R *>(p.res) + row * p.sres, i, lane, p.gs, a[i]);
+      if (valid) store8<VEC>(static_cast<R *>(p.res) + row * p.sres, i, at, p.gs, a[i]);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -60,31 +60,32 @@ __global__ void __launch_bounds__(S::kThreads) norm_fwd_kernel(const Params p) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss[0] = fmaf(a[i][e], a[i][e], ss[0]);
   }
-  row_sum<TPR, 1>(ss, sm);
+  row_sum<S::TPR, 1>(ss, sm);
   const float r = rsqrtf(fmaf(ss[0], p.inv, p.eps));
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     float w[8];
-    load8<float, TPR, VEC>(wr, i, lane, p.gs, true).get(w);
+    load8<VEC>(wr, i, at, p.gs, true).get(w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       a[i][e] *= r * w[e];
       if (MODE == kGateBefore) a[i][e] *= gate[i][e];
     }
     if (valid)
-      store8<T, TPR, VEC>(static_cast<T *>(p.y) + row * p.sy + c0, i, lane, p.gs, a[i]);
+      store8<VEC>(static_cast<T *>(p.y) + row * p.sy + c0, i, at, p.gs, a[i]);
   }
 }
 
 template <typename T, typename R, int MODE>
 cudaError_t launch(const Params &p, bool vec, cudaStream_t stream) {
-  return by_shape(p.gs, [&](auto shape) {
+  return by_shape(p.gs, vec, [&](auto shape) {
     using S = decltype(shape);
     const unsigned grid = static_cast<unsigned>((p.rows * p.ng + S::kRows - 1) / S::kRows);
+    const int threads = S::threads(p.gs);
     if (vec)
-      norm_fwd_kernel<T, R, MODE, S, true><<<grid, S::kThreads, 0, stream>>>(p);
+      norm_fwd_kernel<T, R, MODE, S, true><<<grid, threads, 0, stream>>>(p);
     else
-      norm_fwd_kernel<T, R, MODE, S, false><<<grid, S::kThreads, 0, stream>>>(p);
+      norm_fwd_kernel<T, R, MODE, S, false><<<grid, threads, 0, stream>>>(p);
     return cudaGetLastError();
   });
 }

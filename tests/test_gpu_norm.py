@@ -16,6 +16,8 @@ measured against the larger of the value and of its first term (the second is
 at most sqrt(D) mean |dn o n| <= max |dn| times a factor that the first term
 of some channel reaches).
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -237,3 +239,49 @@ def test_graph_capture_and_other_stream():
     torch.cuda.synchronize()
     for got in outs:
         assert all(torch.equal(got[n], want[n]) for n in want)
+
+
+@pytest.mark.parametrize("width", [16, 128, 512, 640])
+def test_no_epsilon(width):
+    """eps 0 and a number of rows that fills no block: the places behind the
+    last row add nothing to the sums over rows."""
+    r = rnd(width)
+    x, z, w, dy = r(5, width), r(5, width), 1 + 0.1 * r(width), r(5, width)
+    g = sss.gated_rmsnorm_bwd(x, z, w, dy, eps=0.0)
+    lx, lz, lw = (t.to(F64).requires_grad_() for t in (x, z, w))
+    dw, = torch.autograd.grad(gated_rmsnorm(lx, lz, lw, 0.0, width, False), lw, dy.to(F64))
+    assert worst(g["dweight"], dw) <= tol(width, F32, 5)
+    g = sss.add_rmsnorm_bwd(x, w, dy, eps=0.0)
+    lx = x.to(F64).requires_grad_()
+    dw, = torch.autograd.grad(rmsnorm(lx, lw, 0.0), lw, dy.to(F64))
+    assert worst(g["dweight"], dw) <= tol(width, F32, 5)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("width,group", [(320, 16), (1155, 385), (4096, 4096), (16384, 16384)])
+def test_gradient_in_place_of_its_upstream(width, group, dtype):
+    """dx, or dz, in the memory of dy, through the C entry point."""
+    r = rnd(width + group)
+    x, z, dy = (r(600, width).to(dtype) for _ in range(3))
+    w = 1 + 0.1 * r(width)
+    want = sss.gated_rmsnorm_bwd(x, z, w, dy, group_size=group)
+    lib = sss.load_library()
+    for place in ("dx", "dz"):
+        a = sss.GatedNormArgs()
+        a.rows, a.width, a.group_size, a.eps = 600, width, group, 1e-5
+        a.dtype = sss.MSS_F32 if dtype == F32 else sss.MSS_BF16
+        up, other, dw = dy.clone(), torch.empty_like(dy), torch.empty_like(w)
+        a.x, a.z, a.weight, a.dy = x.data_ptr(), z.data_ptr(), w.data_ptr(), up.data_ptr()
+        a.dx, a.dz = (t.data_ptr() for t in ((up, other) if place == "dx" else (other, up)))
+        a.dweight = dw.data_ptr()
+        for n in ("x", "z", "dy", "dx", "dz"):
+            setattr(a, "stride_" + n, width)
+        need = ctypes.c_size_t(0)
+        assert lib.mss_gated_rmsnorm_bwd_workspace_size(ctypes.byref(a), ctypes.byref(need)) == 0
+        ws = torch.empty(need.value, dtype=torch.uint8, device="cuda")
+        a.workspace, a.workspace_bytes = ws.data_ptr(), need.value
+        stream = torch.cuda.current_stream().cuda_stream
+        assert lib.gated_rmsnorm_bwd(ctypes.byref(a), stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(up, want[place]) and torch.equal(dw, want["dweight"])
+        assert torch.equal(other, want["dz" if place == "dx" else "dx"])
