@@ -9,11 +9,20 @@
 //   S_t q = a S_{t-1} q + u (k . q),
 //
 // so the two dot products of a row run beside each other and one round of
-// shuffles over the eight lanes sums both.  A sequence of one token is the
-// decode step: it is bound by reading and writing the fp32 state (8 headdim
-// dstate bytes per head), every load of which is issued before the arithmetic.
-// Over more steps the chain of a step (dots, three shuffles, update) bounds
-// it; the next step's inputs are loaded a step ahead.
+// shuffles over the eight lanes sums both.
+//
+// One token (the decode step) is bound by reading and writing the fp32 state
+// (8 headdim dstate bytes per head), every load of which is issued before the
+// arithmetic: 192 sequences of 32 heads of 128 x 128 take 134 us, 92 % of the
+// copy bandwidth.
+//
+// Over more steps the chain of a step (dots, three shuffles, update) bounds it.
+// What does not hang on the state is kept out of that chain: a tile of TB steps
+// of q, k, v is loaded into registers while the tile before is worked on, then
+// put into shared memory as fp32, where the gates and k . q of its steps are
+// taken by one thread or eight lanes each.  (Loading one step ahead into
+// registers left a step waiting for memory: 227 us for 2 x 517 steps of 6
+// heads of 64 x 64 in fp32, 89 us this way.)
 #include "gated_delta.cuh"
 
 #include <cuda_bf16.h>
@@ -27,8 +36,10 @@ namespace sss48 {
 namespace {
 
 constexpr int kThreads = 128;
-// steps of a sequence (packed ones: on average) from which the chunked
-// evaluation runs
+// Steps of a sequence (packed ones: on average) from which the chunked
+// evaluation runs.  Steps against chunks, us, 32 heads of 128 x 128 in bf16:
+// of one sequence 8.0 / 16.7 at 16 steps, 13.5 / 16.3 at 32, 24 / 16 at 64; of
+// 8 sequences 24 / 33, 42 / 32, 79 / 33; of 32 86 / 119, 156 / 118, 300 / 127.
 constexpr int64_t kChunkSteps = 32;
 constexpr int kGroups = kThreads / 8;  // rows of a block side by side
 
@@ -55,22 +66,12 @@ __device__ __forceinline__ float sum8(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 4);
 }
 
-template <typename InT, typename OutT, int NV, int RPT, bool VEC>
-__global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(const DeltaParams p) {
-  const int nrb = static_cast<int>((p.P + kGroups * RPT - 1) / (kGroups * RPT));
-  const int64_t sh = blockIdx.x / nrb;
-  const int rb = static_cast<int>(blockIdx.x - sh * nrb);
-  const int64_t s = sh / p.H;
-  const int h = static_cast<int>(sh - s * p.H);
-  const int g = h / static_cast<int>(p.H / p.G);
-  const int lane8 = threadIdx.x & 7;
-  const int row0 = rb * kGroups * RPT + (threadIdx.x >> 3);
-  const int N = static_cast<int>(p.N), P = static_cast<int>(p.P);
-  int64_t b, t0, t1;
-  delta_span(p, s, b, t0, t1);
-
-  const int64_t base = sh * p.P * p.N;
-  float4 S[RPT][NV];
+// the thread's part of the state at `src` (NULL: zeros).  It is read once and
+// written once: streaming accesses keep it from displacing the other inputs in
+// the caches.
+template <int NV, int RPT, bool VEC>
+__device__ __forceinline__ void load_state(float4 (&S)[RPT][NV], const float *src, int row0, int P,
+                                           int N, int lane8) {
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     const int row = row0 + r * kGroups;
@@ -78,112 +79,240 @@ __global__ void __launch_bounds__(kThreads) delta_recurrent_kernel(const DeltaPa
     for (int c = 0; c < NV; ++c) {
       const int col = c * 32 + lane8 * 4;
       S[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.h0 && row < P) {
-        const float *src = p.h0 + base + static_cast<int64_t>(row) * N;
+      if (src && row < P) {
+        const float *at = src + static_cast<int64_t>(row) * N;
         if constexpr (VEC) {
-          // read once and written once: streaming accesses keep the state
-          // from displacing the other inputs in the caches
-          if (col < N) S[r][c] = __ldcs(reinterpret_cast<const float4 *>(src + col));
+          if (col < N) S[r][c] = __ldcs(reinterpret_cast<const float4 *>(at + col));
         } else {
-          S[r][c] = row4<float, false>(src, col, N);
+          S[r][c] = row4<float, false>(at, col, N);
         }
       }
     }
   }
-
-  const float A2 = p.A[h] * kLog2e;
-  const float bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-  const InT *qp = static_cast<const InT *>(p.q) + b * p.sq[0] + g * p.sq[2];
-  const InT *kp = static_cast<const InT *>(p.k) + b * p.sk[0] + g * p.sk[2];
-  const InT *vp = static_cast<const InT *>(p.v) + b * p.sv[0] + h * p.sv[2];
-  const InT *dtp = static_cast<const InT *>(p.dt) + b * p.sdt[0] + h * p.sdt[2];
-  const InT *bp = static_cast<const InT *>(p.beta) + b * p.sbeta[0] + h * p.sbeta[2];
-  OutT *yp = static_cast<OutT *>(p.y) + b * p.sy[0] + h * p.sy[2];
-
-  float4 kn[NV], qn[NV];
-  float vn[RPT], dtn = 0.f, bn = 0.f;
-  auto load = [&](int64_t t) {
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      kn[c] = row4<InT, VEC>(kp + t * p.sk[1], c * 32 + lane8 * 4, N);
-      qn[c] = row4<InT, VEC>(qp + t * p.sq[1], c * 32 + lane8 * 4, N);
-    }
-#pragma unroll
-    for (int r = 0; r < RPT; ++r)
-      vn[r] = row0 + r * kGroups < P ? to_f32<InT>(vp[t * p.sv[1] + row0 + r * kGroups]) : 0.f;
-    dtn = to_f32<InT>(dtp[t * p.sdt[1]]);
-    bn = to_f32<InT>(bp[t * p.sbeta[1]]);
-  };
-  if (t0 < t1) load(t0);
-
-  for (int64_t t = t0; t < t1; ++t) {
-    float4 k[NV], q[NV];
-    float v[RPT];
-#pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      k[c] = kn[c];
-      q[c] = qn[c];
-    }
-#pragma unroll
-    for (int r = 0; r < RPT; ++r) v[r] = vn[r];
-    float g2, beta;
-    delta_gates<InT>(p, dtn, bn, A2, bias, g2, beta);
-    if (t + 1 < t1) load(t + 1);
-    const float a = ex2_mufu(g2);
-    float kq = 0.f, sk[RPT], sq[RPT];
-#pragma unroll
-    for (int c = 0; c < NV; ++c) kq = dot4(k[c], q[c], kq);
-#pragma unroll
-    for (int r = 0; r < RPT; ++r) {
-      sk[r] = 0.f;
-      sq[r] = 0.f;
-#pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        sk[r] = dot4(S[r][c], k[c], sk[r]);
-        sq[r] = dot4(S[r][c], q[c], sq[r]);
-      }
-    }
-    kq = sum8(kq);
-#pragma unroll
-    for (int r = 0; r < RPT; ++r) {
-      sk[r] = sum8(sk[r]);
-      sq[r] = sum8(sq[r]);
-    }
-#pragma unroll
-    for (int r = 0; r < RPT; ++r) {
-      const float u = beta * (v[r] - a * sk[r]);
-#pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        S[r][c].x = fmaf(u, k[c].x, a * S[r][c].x);
-        S[r][c].y = fmaf(u, k[c].y, a * S[r][c].y);
-        S[r][c].z = fmaf(u, k[c].z, a * S[r][c].z);
-        S[r][c].w = fmaf(u, k[c].w, a * S[r][c].w);
-      }
-      const int row = row0 + r * kGroups;
-      if (lane8 == 0 && row < P)
-        yp[t * p.sy[1] + row] = from_f32<OutT>(p.scale * fmaf(a, sq[r], u * kq));
-    }
-  }
-
-  if (!p.last) return;
+}
+template <int NV, int RPT, bool VEC>
+__device__ __forceinline__ void store_state(const float4 (&S)[RPT][NV], float *dst, int row0, int P,
+                                            int N, int lane8) {
+  if (!dst) return;
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     const int row = row0 + r * kGroups;
     if (row >= P) continue;
-    float *dst = p.last + base + static_cast<int64_t>(row) * N;
+    float *at = dst + static_cast<int64_t>(row) * N;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
       const int col = c * 32 + lane8 * 4;
       if constexpr (VEC) {
-        if (col < N) __stcs(reinterpret_cast<float4 *>(dst + col), S[r][c]);
+        if (col < N) __stcs(reinterpret_cast<float4 *>(at + col), S[r][c]);
       } else {
         const float v[4] = {S[r][c].x, S[r][c].y, S[r][c].z, S[r][c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (col + e < N) dst[col + e] = v[e];
+          if (col + e < N) at[col + e] = v[e];
       }
     }
   }
+}
+
+// k . q, and S k and S q of the thread's rows, over the eight lanes of each
+template <int NV>
+__device__ __forceinline__ float inner(const float4 (&k)[NV], const float4 (&q)[NV]) {
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < NV; ++c) s = dot4(k[c], q[c], s);
+  return sum8(s);
+}
+template <int NV, int RPT>
+__device__ __forceinline__ void readouts(const float4 (&S)[RPT][NV], const float4 (&k)[NV],
+                                         const float4 (&q)[NV], float (&sk)[RPT],
+                                         float (&sq)[RPT]) {
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    sk[r] = sq[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      sk[r] = dot4(S[r][c], k[c], sk[r]);
+      sq[r] = dot4(S[r][c], q[c], sq[r]);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    sk[r] = sum8(sk[r]);
+    sq[r] = sum8(sq[r]);
+  }
+}
+// S <- a S + u k
+template <int NV>
+__device__ __forceinline__ void write_row(float4 (&S)[NV], const float4 (&k)[NV], float a,
+                                          float u) {
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    S[c].x = fmaf(u, k[c].x, a * S[c].x);
+    S[c].y = fmaf(u, k[c].y, a * S[c].y);
+    S[c].z = fmaf(u, k[c].z, a * S[c].z);
+    S[c].w = fmaf(u, k[c].w, a * S[c].w);
+  }
+}
+
+// the place of a thread and the tensors of its sequence and head
+template <typename InT, typename OutT, int RPT> struct Seat {
+  int h, lane8, row0;
+  int64_t base, t0, t1;
+  float A2, bias;
+  const InT *q, *k, *v, *dt, *beta;
+  OutT *y;
+  __device__ __forceinline__ explicit Seat(const DeltaParams &p) {
+    const int nrb = static_cast<int>((p.P + kGroups * RPT - 1) / (kGroups * RPT));
+    const int64_t sh = blockIdx.x / nrb;
+    const int rb = static_cast<int>(blockIdx.x - sh * nrb);
+    const int64_t s = sh / p.H;
+    h = static_cast<int>(sh - s * p.H);
+    const int g = h / static_cast<int>(p.H / p.G);
+    lane8 = threadIdx.x & 7;
+    row0 = rb * kGroups * RPT + (threadIdx.x >> 3);
+    base = sh * p.P * p.N;
+    int64_t b;
+    delta_span(p, s, b, t0, t1);
+    A2 = p.A[h] * kLog2e;
+    bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    q = static_cast<const InT *>(p.q) + b * p.sq[0] + g * p.sq[2];
+    k = static_cast<const InT *>(p.k) + b * p.sk[0] + g * p.sk[2];
+    v = static_cast<const InT *>(p.v) + b * p.sv[0] + h * p.sv[2];
+    dt = static_cast<const InT *>(p.dt) + b * p.sdt[0] + h * p.sdt[2];
+    beta = static_cast<const InT *>(p.beta) + b * p.sbeta[0] + h * p.sbeta[2];
+    y = static_cast<OutT *>(p.y) + b * p.sy[0] + h * p.sy[2];
+  }
+};
+
+// one token of every sequence (not packed)
+template <typename InT, typename OutT, int NV, int RPT, bool VEC>
+__global__ void __launch_bounds__(kThreads) delta_token_kernel(const DeltaParams p) {
+  const int N = static_cast<int>(p.N), P = static_cast<int>(p.P);
+  const Seat<InT, OutT, RPT> at(p);
+  float4 S[RPT][NV], k[NV], q[NV];
+  load_state<NV, RPT, VEC>(S, p.h0 ? p.h0 + at.base : nullptr, at.row0, P, N, at.lane8);
+  float v[RPT], sk[RPT], sq[RPT], g2, beta;
+#pragma unroll
+  for (int c = 0; c < NV; ++c) {
+    k[c] = row4<InT, VEC>(at.k, c * 32 + at.lane8 * 4, N);
+    q[c] = row4<InT, VEC>(at.q, c * 32 + at.lane8 * 4, N);
+  }
+#pragma unroll
+  for (int r = 0; r < RPT; ++r)
+    v[r] = at.row0 + r * kGroups < P ? to_f32<InT>(at.v[at.row0 + r * kGroups]) : 0.f;
+  delta_gates<InT>(p, to_f32<InT>(*at.dt), to_f32<InT>(*at.beta), at.A2, at.bias, g2, beta);
+  const float a = ex2_mufu(g2), kq = inner<NV>(k, q);
+  readouts<NV, RPT>(S, k, q, sk, sq);
+#pragma unroll
+  for (int r = 0; r < RPT; ++r) {
+    const float u = beta * (v[r] - a * sk[r]);
+    write_row<NV>(S[r], k, a, u);
+    const int row = at.row0 + r * kGroups;
+    if (at.lane8 == 0 && row < P) at.y[row] = from_f32<OutT>(p.scale * fmaf(a, sq[r], u * kq));
+  }
+  store_state<NV, RPT, VEC>(S, p.last ? p.last + at.base : nullptr, at.row0, P, N, at.lane8);
+}
+
+// sequences of any length
+template <typename InT, typename OutT, int NV, int RPT, bool VEC>
+__global__ void __launch_bounds__(kThreads) delta_steps_kernel(const DeltaParams p) {
+  constexpr int TB = NV == 8 ? 8 : 16;              // steps of a tile
+  constexpr int kItems = TB * NV * 8 / kThreads;    // of four columns, per thread, of q and of k
+  constexpr int kRows = kGroups * RPT, kVals = TB * kRows / kThreads;
+  __shared__ __align__(16) float ks[2][TB][NV * 32], qs[2][TB][NV * 32];
+  __shared__ float vs[2][TB][kRows];
+  __shared__ __align__(16) float gate[2][TB][4];  // a, b, k . q
+  const int N = static_cast<int>(p.N), P = static_cast<int>(p.P), tid = threadIdx.x;
+  const Seat<InT, OutT, RPT> at(p);
+  const int block0 = at.row0 - (tid >> 3);
+
+  float4 kn[kItems], qn[kItems];
+  float vn[kVals], dtn = 0.f, bn = 0.f;
+  // a tile's part of a thread, towards registers (zeros behind the sequence)
+  auto load = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int item = tid + i * kThreads, col = item % (NV * 8) * 4;
+      const int64_t r = t + item / (NV * 8);
+      const bool in = r < at.t1;
+      kn[i] = row4<InT, VEC>(at.k + (in ? r * p.sk[1] : 0), col, in ? N : 0);
+      qn[i] = row4<InT, VEC>(at.q + (in ? r * p.sq[1] : 0), col, in ? N : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) {
+      const int item = tid + i * kThreads, row = block0 + item % kRows;
+      const int64_t r = t + item / kRows;
+      vn[i] = r < at.t1 && row < P ? to_f32<InT>(at.v[r * p.sv[1] + row]) : 0.f;
+    }
+    if (tid < TB && t + tid < at.t1) {
+      dtn = to_f32<InT>(at.dt[(t + tid) * p.sdt[1]]);
+      bn = to_f32<InT>(at.beta[(t + tid) * p.sbeta[1]]);
+    }
+  };
+  // ... and from there into the buffer, with what follows from them
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int item = tid + i * kThreads;
+      *reinterpret_cast<float4 *>(&ks[buf][0][0] + item * 4) = kn[i];
+      *reinterpret_cast<float4 *>(&qs[buf][0][0] + item * 4) = qn[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kVals; ++i) (&vs[buf][0][0])[tid + i * kThreads] = vn[i];
+    if (tid < TB) {
+      float g2, b;
+      delta_gates<InT>(p, dtn, bn, at.A2, at.bias, g2, b);
+      gate[buf][tid][0] = ex2_mufu(g2);
+      gate[buf][tid][1] = b;
+    }
+    __syncthreads();
+    if ((tid >> 3) < TB) {  // whole warps
+      float4 k[NV], q[NV];
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        k[c] = *reinterpret_cast<const float4 *>(&ks[buf][tid >> 3][c * 32 + at.lane8 * 4]);
+        q[c] = *reinterpret_cast<const float4 *>(&qs[buf][tid >> 3][c * 32 + at.lane8 * 4]);
+      }
+      const float kq = inner<NV>(k, q);
+      if (at.lane8 == 0) gate[buf][tid >> 3][2] = kq;
+    }
+    __syncthreads();
+  };
+
+  if (at.t0 < at.t1) load(at.t0);
+  float4 S[RPT][NV];
+  load_state<NV, RPT, VEC>(S, p.h0 ? p.h0 + at.base : nullptr, at.row0, P, N, at.lane8);
+  if (at.t0 < at.t1) put(0);
+  int buf = 0;
+  for (int64_t t = at.t0; t < at.t1; t += TB, buf ^= 1) {
+    if (t + TB < at.t1) load(t + TB);
+    const int n = at.t1 - t < TB ? static_cast<int>(at.t1 - t) : TB;
+    OutT *yp = at.y + t * p.sy[1];
+#pragma unroll 2
+    for (int j = 0; j < n; ++j) {
+      float4 k[NV], q[NV];
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        k[c] = *reinterpret_cast<const float4 *>(&ks[buf][j][c * 32 + at.lane8 * 4]);
+        q[c] = *reinterpret_cast<const float4 *>(&qs[buf][j][c * 32 + at.lane8 * 4]);
+      }
+      const float a = gate[buf][j][0], beta = gate[buf][j][1], kq = gate[buf][j][2];
+      float sk[RPT], sq[RPT];
+      readouts<NV, RPT>(S, k, q, sk, sq);
+#pragma unroll
+      for (int r = 0; r < RPT; ++r) {
+        const float u = beta * (vs[buf][j][(tid >> 3) + r * kGroups] - a * sk[r]);
+        write_row<NV>(S[r], k, a, u);
+        const int row = at.row0 + r * kGroups;
+        if (at.lane8 == 0 && row < P)
+          yp[j * p.sy[1] + row] = from_f32<OutT>(p.scale * fmaf(a, sq[r], u * kq));
+      }
+    }
+    // (its own syncs order the tiles: the buffer written here was read before
+    // the ones of the last tile)
+    if (t + TB < at.t1) put(buf ^ 1);
+  }
+  store_state<NV, RPT, VEC>(S, p.last ? p.last + at.base : nullptr, at.row0, P, N, at.lane8);
 }
 
 bool al(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -191,11 +320,17 @@ bool al(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) =
 template <typename InT, typename OutT, int NV, int RPT, bool VEC>
 cudaError_t go(const DeltaParams &p, cudaStream_t stream) {
   const int64_t nrb = (p.P + kGroups * RPT - 1) / (kGroups * RPT);
-  delta_recurrent_kernel<InT, OutT, NV, RPT, VEC>
-      <<<static_cast<unsigned>(p.seqs * p.H * nrb), kThreads, 0, stream>>>(p);
+  const unsigned grid = static_cast<unsigned>(p.seqs * p.H * nrb);
+  if (p.L == 1 && !p.cu)
+    delta_token_kernel<InT, OutT, NV, RPT, VEC><<<grid, kThreads, 0, stream>>>(p);
+  else
+    delta_steps_kernel<InT, OutT, NV, RPT, VEC><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
+// Two rows of a thread share its k and q (one row in twice the blocks: 8
+// sequences of 64 steps of 32 heads of 128 x 128, 111 us against 84; it is 5 %
+// faster where there are few blocks); at dstate 256 two would not fit.
 template <typename InT, typename OutT, bool VEC>
 cudaError_t by_size(const DeltaParams &p, cudaStream_t stream) {
   if (p.N <= 64) return go<InT, OutT, 2, 2, VEC>(p, stream);
@@ -243,7 +378,7 @@ mss_status check_sizes(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t G
   // sizes whose grid, 32-bit tensor coordinates or row index would overflow
   const int64_t lim = int64_t(1) << 30;
   if (P > lim || H > lim || L > lim || batch > lim || batch > lim / H ||
-      batch * H > lim / ((P + 15) / 16))
+      batch * H > lim / ((P + kGroups - 1) / kGroups))
     return MSS_ERR_UNSUPPORTED;
   return MSS_OK;
 }
