@@ -31,6 +31,8 @@
  *              S = e^(c_last) H0 + U^T diag(e^(c_last - c)) K.  Operands that
  *              are not bf16 already enter the products as the sum of two
  *              bf16 values, so the result keeps about 16 bits.
+ * A NaN or an infinity in a step's inputs spoils that head from the step on
+ * (recurrent) or from the first step of its chunk on (chunked), nothing else.
  *
  * Layouts (the last dimension contiguous; batch, step and head strides in
  * elements are given per tensor, so views of a wider projection are read in

@@ -18,7 +18,7 @@ import pytest
 import torch
 
 import selective_state_space_48_b200 as sss
-from delta_checks import delta_inputs, gated_delta, worst
+from delta_checks import delta_inputs, gated_delta, gated_rmsnorm, worst
 
 pytestmark = pytest.mark.gpu
 
@@ -223,3 +223,146 @@ def test_state_in_place_other_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(state, want) and torch.equal(y, want_y)
+
+
+def projection(batch, L, H, P, G, N, seed=0):
+    """q, k, v as slices of one wide bf16 projection, and the same dense."""
+    d = delta_inputs(batch, L, H, P, G, N, BF, seed=seed, h0=True)
+    parts = [d[n].flatten(2) for n in ("q", "k", "v")]
+    wide = torch.cat([parts[0], torch.zeros_like(parts[0][..., :8]), *parts[1:]], -1)
+    q, _, k, v = wide.split([G * N, 8, G * N, H * P], -1)
+    views = dict(d, q=q.unflatten(2, (G, N)), k=k.unflatten(2, (G, N)), v=v.unflatten(2, (H, P)))
+    return d, views
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("shift", [0, 1, 8])
+def test_chunked_views_of_a_projection(out_dtype, shift):
+    """Strided q, k, v and a strided y, whose rows start on 16 bytes (they
+    leave through tensor maps in bf16) or do not: the bits of dense copies,
+    and nothing written beside y."""
+    d, views = projection(2, 150, 4, 64, 2, 64)
+    want, wl = sss.gated_delta_fwd(**d, return_last_state=True, out_dtype=out_dtype, plan=2)
+    buf = torch.full((2, 150, 4, 80), 7.0, device="cuda", dtype=out_dtype)
+    y = buf[..., shift:shift + 64]
+    got, gl = sss.gated_delta_fwd(**views, return_last_state=True, y=y, plan=2)
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    assert (buf[..., :shift] == 7).all() and (buf[..., shift + 64:] == 7).all()
+
+
+@pytest.mark.parametrize("headdim", [64, 72, 136, 192])
+def test_chunked_packed_bf16_rows(headdim):
+    """Rows behind the last sequence stay as they were, bf16 y included, for
+    widths that fill their 64-wide and 128-wide tiles or do not."""
+    cu = torch.tensor([0, 64, 64, 65, 200, 328, 330], dtype=torch.int32, device="cuda")
+    d = delta_inputs(1, 340, 2, headdim, 1, 64, BF, h0=True, seqs=6)
+    y = torch.full((1, 340, 2, headdim), 7.0, device="cuda", dtype=BF)
+    check(d, "chunked", BF, cu_seqlens=cu, y=y)
+    assert (y[0, 330:] == 7.0).all()
+
+
+@pytest.mark.parametrize("seqs", [7, 890, 1000])
+def test_chunked_many_sequences(seqs):
+    """Sequences are taken longest first up to a number of them and in their
+    own order beyond: every one is done, equal lengths among them."""
+    lens = torch.tensor([(i * 7) % 5 for i in range(seqs)])
+    lens[seqs // 2] = 130
+    cu = torch.cat([torch.zeros(1, dtype=torch.long), lens.cumsum(0)]).to(torch.int32).cuda()
+    d = delta_inputs(1, int(cu[-1]), 2, 64, 1, 64, BF, h0=True, seqs=seqs)
+    y, last = sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=True, plan=2)
+    yr, lr = sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=True, plan=1)
+    assert worst(y, yr) <= tolerance(64, 130, F32, True) + tolerance(64, 130)
+    assert worst(last, lr) <= tolerance(64, 130, F32, True) + tolerance(64, 130)
+
+
+@pytest.mark.parametrize("n", ["q", "k", "v", "dt", "beta"])
+def test_non_finite_steps_stay_in_their_head_and_chunk(n):
+    """A NaN in a step of a head reaches that head's rows from the start of
+    its 64-step chunk on (chunked) or from its step on (recurrent), and
+    nothing else."""
+    d = delta_inputs(2, 200, 4, 64, 4, 64, BF)
+    want = {p: sss.gated_delta_fwd(**d, plan=p) for p in (1, 2)}
+    d[n][1, 100, 2] = float("nan")
+    for plan, first in ((1, 100), (2, 64)):
+        y = sss.gated_delta_fwd(**d, plan=plan)
+        assert torch.isnan(y[1, 100, 2]).any()
+        same = torch.ones(2, 200, 4, dtype=torch.bool, device="cuda")
+        same[1, first:, 2] = False
+        assert torch.equal(y[same], want[plan][same])
+
+
+def test_plan_follows_the_length():
+    for L, plan in ((31, 1), (32, 2)):
+        d = delta_inputs(2, L, 2, 64, 1, 64, BF)
+        assert torch.equal(sss.gated_delta_fwd(**d), sss.gated_delta_fwd(**d, plan=plan))
+    d = delta_inputs(1, 64, 2, 64, 1, 64, BF, seqs=4)
+    cu = torch.tensor([0, 61, 62, 63, 64], dtype=torch.int32, device="cuda")  # 16 on average
+    kw = dict(cu_seqlens=cu)
+    assert torch.equal(sss.gated_delta_fwd(**d, **kw), sss.gated_delta_fwd(**d, plan=1, **kw))
+
+
+@pytest.mark.parametrize("plan", [1, 2])
+def test_two_calls_at_once_and_two_graphs(plan):
+    """Calls on two streams at the same time, then two graphs of the same
+    tensors, replayed twice: the bits of a call alone."""
+    d = [delta_inputs(4, 150, 8, 64, 2, 64, BF, seed=s, h0=True) for s in (1, 2)]
+    want = [sss.gated_delta_fwd(**x, return_last_state=True, plan=plan) for x in d]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in d]
+    for _ in range(5):
+        got = [sss.gated_delta_fwd(**x, return_last_state=True, plan=plan, stream=s)
+               for x, s in zip(d, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    graphs, outs = [], []
+    for x in d:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(sss.gated_delta_fwd(**x, return_last_state=True, plan=plan))
+        graphs.append(graph)
+    for graph in graphs * 2:
+        graph.replay()
+    torch.cuda.synchronize()
+    for g, w in zip(outs, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_layer():
+    """The operators as a layer uses them: the norm with the residual sum, a
+    projection whose slices go into the delta rule in place, the gated norm
+    per head; a prompt, then single tokens from its state.  Every stage is
+    compared with float64 of what entered it."""
+    B, L, H, P, G, N, D = 2, 70, 4, 64, 2, 64, 256
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    widths = [G * N, G * N, H * P, H * P, H, H]
+    w_in = (rnd(D, sum(widths)) / 16).to(BF)
+    w1, w2, scale = 1 + 0.1 * rnd(D), 1 + 0.1 * rnd(P), 0.5 + 0.1 * rnd(D)
+    A, bias = -1 - 15 * torch.rand(H, generator=g, device="cuda"), rnd(H) - 4
+    state = torch.zeros(B, H, P, N, device="cuda")
+    want_state = state.double()
+    unit = lambda t: torch.nn.functional.normalize(t.float(), dim=-1).to(BF)  # noqa: E731
+    for steps in (L, 1, 1):
+        x, res = rnd(B, steps, D).to(BF), rnd(B, steps, D)
+        h, total = sss.add_rmsnorm_fwd(x, res, w1, scale=scale)
+        want = x.double() * scale + res
+        assert worst(total, want) <= 2.0 ** -23
+        want = total.double() / torch.sqrt(total.double().pow(2).mean(-1, keepdim=True) + 1e-5)
+        assert worst(h, want * w1) <= 2.0 ** -8 + 64 * 2.0 ** -24
+        wide = h @ w_in
+        wide[..., :2 * G * N] = unit(wide[..., :2 * G * N].unflatten(-1, (-1, N))).flatten(-2)
+        q, k, v, z, dt, beta = wide.split(widths, -1)
+        q, k, v = (q.unflatten(-1, (G, N)), k.unflatten(-1, (G, N)), v.unflatten(-1, (H, P)))
+        if steps > 1:
+            y, _ = sss.gated_delta_fwd(q, k, v, dt, A, beta, bias, h0=state, last_state=state,
+                                       return_last_state=True, out_dtype=BF, check_status=True)
+        else:
+            y = sss.gated_delta_update(state, q[:, 0], k[:, 0], v[:, 0], dt[:, 0], A, beta[:, 0],
+                                       bias, out_dtype=BF)[:, None]
+        yr, want_state = gated_delta(q, k, v, dt, A, beta, bias, h0=want_state)
+        assert worst(y, yr) <= tolerance(N, L + 2, BF, True)
+        assert worst(state, want_state) <= tolerance(N, L + 2, F32, True)
+        o = sss.gated_rmsnorm_fwd(y.flatten(-2), z, w2, group_size=P)
+        want = gated_rmsnorm(y.flatten(-2).double(), z.double(), w2.double(), 1e-5, P, False)
+        assert worst(o, want) <= 2.0 ** -8 + 64 * 2.0 ** -24

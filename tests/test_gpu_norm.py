@@ -285,3 +285,17 @@ def test_gradient_in_place_of_its_upstream(width, group, dtype):
         torch.cuda.synchronize()
         assert torch.equal(up, want[place]) and torch.equal(dw, want["dweight"])
         assert torch.equal(other, want["dz" if place == "dx" else "dx"])
+
+
+def test_parameters_as_weights():
+    r = rnd(8)
+    x, z = r(3, 64).requires_grad_(), r(3, 64)
+    w, s = (torch.nn.Parameter(1 + 0.1 * r(64)) for _ in range(2))
+    y, out = sss.add_rmsnorm_fn(x, z, w, scale=s)
+    o = sss.gated_rmsnorm_fn(y, out, w)
+    dx, dw, ds = torch.autograd.grad(o.sum(), (x, w, s))
+    lx, lw, ls = (t.detach().to(F64).requires_grad_() for t in (x, w, s))
+    total = lx * ls + z
+    want = gated_rmsnorm(rmsnorm(total, lw, 1e-5), total, lw, 1e-5, 64, False).sum()
+    for a, b in zip((dx, dw, ds), torch.autograd.grad(want, (lx, lw, ls))):
+        assert worst(a, b) <= 4 * tol(64, F32, 3)
