@@ -42,7 +42,7 @@
 //                 them longer than the chain takes for one
 // The inverse: 16 x 16 triangles by substitution, a column per lane, then the
 // blocks below them as products, -T22 (A21 T11), in fp32 (2 x 4 values of a
-// thread; the same as three tf32 mma.sync products took 2.2 us more of a chunk).
+// thread; as three tf32 mma.sync products they made a chunk 2.2 us longer).
 //
 // Shared memory tiles are rows of 128 bytes with the 128-byte swizzle.  Every
 // wait is bounded as in tcgen05.cuh, so no block can hang.
@@ -79,7 +79,7 @@ constexpr int kGate = 2 * C * 4;
 constexpr int oDecay = oGate + 2 * kGate;  // three of (2^(c_last - c), 2^c, scale 2^c) [C]
 constexpr int kDecay = 3 * C * 4;
 constexpr int oBar = oDecay + 3 * kDecay;
-constexpr int kBars = 35;
+constexpr int kBars = 36;
 constexpr int oTmemSlot = oBar + kBars * 8;
 constexpr int oAbort = oTmemSlot + 4;
 constexpr int oSeq = oAbort + 4;
@@ -98,29 +98,36 @@ constexpr uint32_t kColS = 448;   // K K^T (lanes 0..63), Q K^T (64..127)
 constexpr uint32_t kTmemCols = 512;
 
 // Barriers.  Tiles landed and released; per chunk, products done (S, X, U, O1,
-// the update, O) and operands ready (H; R; U'; U; T and P), S and O drained; y staged; the two P buffers released; the gates written (the decays have three buffers, the rest
-// two) and their two and three buffers released.  A waiter may not fall two
-// phases behind: where it could, the barriers are a ring.  The groups arrive
-// one lane per warp.
+// the update, O) and operands ready (H; R; U'; U; T and P), S and O drained; y
+// staged; the two P buffers released; the gates written (the decays have three
+// buffers, the rest two) and their two and three buffers released; every
+// product done.  A waiter may not fall two phases behind: where it could, the
+// barriers are a ring.  The groups arrive one lane per warp.  (H, R and U' in
+// four parts, so that a product starts with the first of them, cost more in
+// waits than they gained: 618 us against 482 for 8192 steps.)
 constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 9, kDoneX = 11,
               kDoneU = 12, kDoneO1 = 13, kDoneH = 14, kDoneO = 15, kReadyH = 16, kReadyR = 17,
               kReadyU = 18, kReadyO = 19, kFreeO = 20, kReadyY = 21, kFreeS = 22, kReadyT = 23,
-              kFreeP = 25, kReadyG = 27, kFreeG = 30, kFreeD = 32;  // .. 34
+              kFreeP = 25, kReadyG = 27, kFreeG = 30, kFreeD = 32,
+              kEnd = 35;
 // arrivals that complete a barrier's phase
 __device__ __forceinline__ int bar_count(int i) {
   if (i == kFreeS || i == kReadyT || i == kReadyT + 1 || i == kFreeG || i == kFreeG + 1)
     return kAuxWarps;
-  if ((i >= kReadyH && i <= kReadyY) || i >= kFreeD)
-    return kChainWarps;
+  if ((i >= kReadyH && i <= kReadyY) || (i >= kFreeD && i < kEnd)) return kChainWarps;
   return 1;
 }
 
 // Bounded waits, short since every one is inlined: instructions from beyond
-// the instruction caches were what bounded a longer form of this kernel.  A
+// the instruction caches bound this kernel where every SM runs it (108 KB of
+// code took twice the time; 78 KB, with the products unrolled, 292 us for 8 x
+// 2048 steps, 71 KB, with them in loops, 275, though alone on its SMs the
+// longer form is 2 % faster).  A
 // wait gives up after `limit` tries, each of which suspends the thread for up
 // to kTryNs; then, and once any wait of the block has given up, every wait
-// that is not complete returns (the results are garbage, but nothing hangs),
-// and the block's end records the timeout.
+// that is not complete returns (the results are garbage, but nothing hangs:
+// products run on whatever their operands hold), and the block's end records
+// the timeout.
 constexpr uint32_t kTryNs = 20000;
 struct Waits {
   uint32_t bar;  // shared-memory address of the barriers
@@ -357,8 +364,9 @@ __device__ __forceinline__ constexpr uint32_t kslice(int k) {
 }
 
 // NK: 16-wide slices of dstate (4 up to 64, else 8; TMA pads with zeros).
-// y_tma: whole chunks of y go out through their Q tile and a TMA store (bf16 rows that a tensor map takes): 16 two-byte
-// stores of a thread straight to memory took 1.3 us of a chunk's 4.5.
+// y_tma: whole chunks of y go out through their Q tile and a TMA store (bf16
+// rows that a tensor map takes): 16 two-byte stores of a thread straight to
+// memory took 1.3 us of a chunk's 4.5.
 template <typename OutT, int NK>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p, const int y_tma) {
@@ -425,10 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer
     if (lane == 0) {
-      for (int i = 0; i < nc; ++i) {
+      int i = 0;
+      for (; i < nc; ++i) {
         const int t = static_cast<int>(t0) + i * C;
         const int a = i % 3;
         if (i >= 3) sy.wait(kEmptyKQ + a, (i / 3 - 1) & 1);
+        if (*abort) break;  // (the waits are no order any more)
         unsigned char *d = sm + oKQ + a * kStageKQ;
         mbar_expect_tx(bar + kFullKQ + a, kStageKQ);
         tma_load_4d(d, &maps.k, 0, g, t, b, bar + kFullKQ + a);
@@ -437,14 +447,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_4d(d + 3 * kHalf, &maps.q, 64, g, t, b, bar + kFullKQ + a);
       }
       // no copy may still be landing when the block exits
-      for (int i = nc > 3 ? nc - 3 : 0; i < nc; ++i) sy.drain(kFullKQ + i % 3, (i / 3) & 1);
+      for (int j = i > 3 ? i - 3 : 0; j < i; ++j) sy.drain(kFullKQ + j % 3, (j / 3) & 1);
     }
     __syncwarp();
   } else if (warp == 3) {
     // (V waits for its one place, while K and Q run ahead)
     if (lane == 0) {
-      for (int i = 0; i <= nc; ++i) {
+      int i = 0;  // V of chunk i, y of the one before
+      for (; i <= nc; ++i) {
         if (i > 0) sy.wait(kEmptyV, (i - 1) & 1);
+        if (*abort) break;
         if (i < nc) {
           const int t = static_cast<int>(t0) + i * C;
           uint64_t *full = bar + kFullV + (i & 1);
@@ -465,26 +477,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_store_wait_read();
         mbar_arrive(bar + kEmptyKQ + a);
       }
-      for (int i = nc > 2 ? nc - 2 : 0; i < nc; ++i) sy.drain(kFullV + (i & 1), (i / 2) & 1);
+      const int loads = min(i, nc);
+      for (int j = loads > 2 ? loads - 2 : 0; j < loads; ++j)
+        sy.drain(kFullV + (j & 1), (j / 2) & 1);
       tma_store_wait_all();
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------- tensor-core issue
     const uint32_t on = elect_one();
-    // after a timeout nothing is issued any more (commits still complete)
-    auto alive = [&]() { return !__any_sync(0xffffffffu, *abort); };
     auto ready = [&](int i, uint32_t parity) {
       return __shfl_sync(0xffffffffu, sy.test(i, parity), 0) != 0;
     };
     int ns = 0, sst = 0;  // the next chunk whose S = [K; Q] K^T is due, ns % 3
     auto issue_scores = [&]() {
       tc_fence_after();
-      if (alive()) {
-        const uint32_t d = desc_lo(sbase + oKQ + sst * kStageKQ, 16);
+      const uint32_t d = desc_lo(sbase + oKQ + sst * kStageKQ, 16);
 #pragma unroll 1
-        for (int k = 0; k < NK; ++k) mma_ss(kColS, d + kslice(k), d + kslice(k), kIdKK, k > 0, on);
-      }
+      for (int k = 0; k < NK; ++k) mma_ss(kColS, d + kslice(k), d + kslice(k), kIdKK, k > 0, on);
       mma_commit(bar + kDoneS + (ns & 1), on);
       ++ns;
       sst = sst == 2 ? 0 : sst + 1;
@@ -504,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       sy.wait(kReadyH, i & 1);
       tc_fence_after();
-      if (alive()) {  // X = H K^T
+      {  // X = H K^T
         const uint32_t dK = desc_lo(kq, 16);
-#pragma unroll 2
+#pragma unroll 2  // (rolled: what the instruction caches hold, see the waits)
         for (int k = 0; k < NK; ++k) {
           const uint32_t hi = kColH + (k >> 1) * 32 + (k & 1) * 8;
           mma_ts(kColX, hi, dK + kslice(k), kIdKK, k > 0, on);
@@ -526,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sy.wait(kFullV + (i & 1), (i / 2) & 1);
       if (i > 0) sy.wait(kDoneO, (i - 1) & 1);  // U of the chunk before has been read
       tc_fence_after();
-      if (alive()) {  // U^T = V^T T^T
+      {  // U^T = V^T T^T
         const uint32_t dV = desc_lo(sbase + oV, kHalf);
 #pragma unroll 2
         for (int k = 0; k < 4; ++k) {
@@ -537,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(bar + kEmptyV, on);
       sy.wait(kReadyR, i & 1);
       tc_fence_after();
-      if (alive()) {  // U^T += R^T T^T
+      {  // U^T += R^T T^T
 #pragma unroll 2
         for (int k = 0; k < 4; ++k) {
           mma_ts(kColU, kColX + 16 * k, dT + k * 2, kIdKK, 1, on);
@@ -546,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mma_commit(bar + kDoneU, on);
-      if (alive()) {  // O1 = H Q^T
+      {  // O1 = H Q^T
         const uint32_t dQ = desc_lo(kq + kHalf, 16), o1 = kColO1 + (i & 1) * 64;
 #pragma unroll 2
         for (int k = 0; k < NK; ++k) {
@@ -560,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sy.wait(kDoneO1, i & 1);  // the update overwrites the pairs of H
       sy.wait(kReadyU, i & 1);
       tc_fence_after();
-      if (alive()) {  // U'^T K
+      {  // U'^T K
         const uint32_t dK = desc_lo(kq, 2 * kHalf);
 #pragma unroll 2
         for (int k = 0; k < 4; ++k) {
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i > 0) sy.wait(kFreeO, (i - 1) & 1);
       sy.wait(kReadyO, i & 1);
       tc_fence_after();
-      if (alive()) {  // O2 = U^T (Q K^T o D)^T
+      {  // O2 = U^T (Q K^T o D)^T
         const uint32_t dP = desc_lo(sbase + oP + (i & 1) * 2 * kHalf, 16);
 #pragma unroll 2
         for (int k = 0; k < 4; ++k) {
@@ -590,6 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // arrived, those too that nobody waits for: an arrival at the shared
     // memory of a block that has ended is an illegal access
     if (nc > 0) {
+      // (after a timeout the waits above were no order any more: this one,
+      // used once, is behind everything)
+      mma_commit(bar + kEnd, on);
+      sy.drain(kEnd, 0);
       sy.drain(kDoneO, (nc - 1) & 1);
       sy.drain(kEmptyV, (nc - 1) & 1);
       for (int i = y_tma ? nc : (nc > 3 ? nc - 3 : 0); i < nc; ++i)
@@ -735,18 +749,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i > 0) update(i - 1);
       if (i < nc) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t hi[8], lo[8];
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split2(H[16 * c + 2 * j], H[16 * c + 2 * j + 1], hi[j], lo[j]);
-        tmem_st8(tl + kColH + 32 * e + 8 * c, hi);
-        tmem_st8(tl + kColH + 32 * e + 16 + 8 * c, lo);
+          for (int j = 0; j < 8; ++j)
+            split2(H[16 * c + 2 * j], H[16 * c + 2 * j + 1], hi[j], lo[j]);
+          tmem_st8(tl + kColH + 32 * e + 8 * c, hi);
+          tmem_st8(tl + kColH + 32 * e + 16 + 8 * c, lo);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        warp_arrive(bar + kReadyH, lane);
+        sy.wait(kReadyG + i % 3, (i / 3) & 1);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      warp_arrive(bar + kReadyH, lane);
-      }
-      if (i < nc) sy.wait(kReadyG + i % 3, (i / 3) & 1);
       if (i > 0) output(i - 1);
       if (i >= nc) break;
 
