@@ -850,27 +850,30 @@ def _enqueue(name, packed, device, stream):
         raise MssError(rc, name)
 
 
-def _alike(t, dtype, device, shape):
-    """A tensor of this dtype, device and shape whose rows are contiguous."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
-            and t.shape == shape and (t.stride(-1) == 1 or shape[-1] == 1))
+_Tensor = torch.Tensor
+
+
+def _tensors(a, b, c, d):
+    return (isinstance(a, _Tensor) and isinstance(b, _Tensor) and isinstance(c, _Tensor)
+            and isinstance(d, _Tensor))
 
 
 def _dense(t, dtype, device, shape):
-    return t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+    return t is None or (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device
                          and t.shape == shape and t.is_contiguous())
 
 
 def _new(like, dtype=None):
     """An uninitialised contiguous tensor of the shape and device of `like`."""
-    if like.is_contiguous():  # (half the time of torch.empty)
-        return torch.empty_like(like) if dtype is None or dtype is like.dtype else \
-            torch.empty_like(like, dtype=dtype)
-    return torch.empty(like.shape, dtype=dtype or like.dtype, device=like.device)
+    if dtype is None or dtype is like.dtype:
+        if like.is_contiguous():  # (half the time of torch.empty)
+            return torch.empty_like(like)
+        dtype = like.dtype
+    return torch.empty(like.shape, dtype=dtype, device=like.device)
 
 
 def _same(t, dtype, device, shape):
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+    return (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device
             and t.shape == shape)
 
 
@@ -893,10 +896,13 @@ def _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scal
             raise ValueError("packed sequences need batch 1")
         seqs, cu = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
     states = (seqs, H, P, N)
-    if not (dev.type == "cuda" and _alike(q, ind, dev, keys) and _alike(k, ind, dev, keys)
-            and _alike(v, ind, dev, values) and (y is None or _alike(y, y.dtype, dev, values))
-            and _same(dt, ind, dev, heads) and _same(beta, ind, dev, heads)
-            and A is not None and _dense(A, f32, dev, (H,)) and _dense(dt_bias, f32, dev, (H,))
+    if not (_tensors(k, dt, beta, A) and q.is_cuda
+            and ind is k.dtype is v.dtype is dt.dtype is beta.dtype
+            and dev == k.device == v.device == dt.device == beta.device
+            and q.shape == keys == k.shape and dt.shape == heads == beta.shape
+            and q.stride()[3] == k.stride()[3] == v.stride()[3] == 1
+            and (y is None or (_same(y, y.dtype, dev, values) and y.stride()[3] == 1))
+            and _dense(A, f32, dev, (H,)) and _dense(dt_bias, f32, dev, (H,))
             and _dense(h0, f32, dev, states) and _dense(last_state, f32, dev, states)):
         _check_views(dev, [
             ("q", q, ind, keys, "rows"), ("k", k, ind, keys, "rows"),
@@ -975,7 +981,7 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
     nheads, headdim, dstate) float32 is updated in place.  q, k: (batch,
     ngroups, dstate); v: (batch, nheads, headdim); dt, beta: (batch, nheads);
     views as for ``gated_delta_fwd``.  Returns y (batch, nheads, headdim)."""
-    if not all(isinstance(t, torch.Tensor) for t in (state, q, v)):
+    if not _tensors(state, q, v, state):
         raise TypeError("state, q and v must be CUDA tensors")
     if state.dim() != 4 or q.dim() != 3:
         raise ValueError("state must be (batch, heads, headdim, dstate), q (batch, groups, dstate)")
@@ -984,10 +990,13 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
     if y is None:
         y = _new(v, out_dtype)
     keys, values, heads = (batch, G, N), (batch, H, P), (batch, H)
-    if not (dev.type == "cuda" and _alike(q, ind, dev, keys) and _alike(k, ind, dev, keys)
-            and _alike(v, ind, dev, values) and _alike(y, y.dtype, dev, values)
-            and _same(dt, ind, dev, heads) and _same(beta, ind, dev, heads)
-            and _dense(state, f32, dev, shape) and A is not None and _dense(A, f32, dev, (H,))
+    if not (_tensors(k, dt, beta, A) and isinstance(y, _Tensor) and q.is_cuda
+            and ind is k.dtype is v.dtype is dt.dtype is beta.dtype
+            and dev == k.device == v.device == dt.device == beta.device == y.device
+            and q.shape == keys == k.shape and v.shape == values == y.shape
+            and dt.shape == heads == beta.shape
+            and q.stride()[2] == k.stride()[2] == v.stride()[2] == y.stride()[2] == 1
+            and _dense(state, f32, dev, shape) and _dense(A, f32, dev, (H,))
             and _dense(dt_bias, f32, dev, (H,))):
         _check_views(dev, [
             ("state", state, f32, None, "dense"), ("q", q, ind, keys, "rows"),
@@ -999,8 +1008,8 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
         batch, H, P, G, N, _dtype_code(ind), _dtype_code(y.dtype), state.data_ptr(),
         q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), A.data_ptr(), beta.data_ptr(),
         0 if dt_bias is None else dt_bias.data_ptr(), bool(dt_softplus), bool(beta_sigmoid),
-        N ** -0.5 if scale is None else float(scale), y.data_ptr(), *q.stride()[:2], *k.stride()[:2],
-        *v.stride()[:2], *dt.stride(), *beta.stride(), *y.stride()[:2])
+        N ** -0.5 if scale is None else float(scale), y.data_ptr(), *q.stride()[:2],
+        *k.stride()[:2], *v.stride()[:2], *dt.stride(), *beta.stride(), *y.stride()[:2])
     _enqueue("gated_delta_update", packed, dev, stream)
     return y
 
@@ -1032,16 +1041,17 @@ def _rows_of(name, t):
 def _norm_rows(device, shape, named):
     """[pointer, ...] and [row stride, ...] of the (..., width) tensors of a
     norm call (0 for None)."""
-    ptrs, strides = [], []
+    ptrs, strides, width = [], [], shape[-1]
     for name, t, dtype in named:
         if t is None:
             ptrs.append(0)
             strides.append(0)
             continue
-        if not (_same(t, dtype, device, shape) and device.type == "cuda"):
+        if not (isinstance(t, _Tensor) and t.is_cuda and t.dtype is dtype and t.device == device
+                and t.shape == shape):
             _check_views(device, [(name, t, dtype, shape, "rows")])
         ptrs.append(t.data_ptr())
-        strides.append(shape[-1] if t.is_contiguous() else _rows_of(name, t)[1])
+        strides.append(width if t.is_contiguous() else _rows_of(name, t)[1])
     return ptrs, strides
 
 

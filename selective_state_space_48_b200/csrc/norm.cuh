@@ -42,16 +42,18 @@ struct Params {
 // a block of 128.  Longer rows (TPR 0): a block per row, as many threads as it
 // takes at NV pieces each, at most 512 (2560 channels are 160 threads: with a
 // power of two the spare ones cost a third of the time).
-template <int TPR_, int NV_> struct Shape {
+// MAXT: the most threads of a block per row; kVector: for rows of vectors only.
+template <int TPR_, int NV_, int MAXT_ = 512> struct Shape {
   static constexpr int TPR = TPR_, NV = NV_;
-  static constexpr int kMaxThreads = TPR_ ? 128 : 512;
+  static constexpr int kMaxThreads = TPR_ ? 128 : MAXT_;
+  static constexpr bool kVector = MAXT_ < 512;
   static constexpr int kRows = TPR_ ? 128 / (TPR_ ? TPR_ : 1) : 1;  // rows of a block
   static int threads(int64_t gs) {
     return TPR_ ? 128 : static_cast<int>(((gs + 8 * NV_ - 1) / (8 * NV_) + 31) / 32 * 32);
   }
 };
 // Two pieces of a thread from 1024 channels on where rows move as vectors
-// (16384 rows of 4096 in bf16: forward 66 us, 82 with one piece, backward 140,
+// (16384 rows of 4096 in bf16: forward 66 us, 82 with one piece, backward 129,
 // 157 with one), one where they are scalar (4096 rows of 1155: backward 33 us,
 // 38 with two).
 template <typename F> auto by_shape(int64_t gs, bool vec, F f) {
@@ -59,6 +61,8 @@ template <typename F> auto by_shape(int64_t gs, bool vec, F f) {
   if (gs <= 128) return f(Shape<16, 1>());
   if (gs <= 512) return f(Shape<32, 2>());
   if (gs <= (vec ? 1024 : 4096)) return f(Shape<0, 1>());
+  if (vec && gs <= 4096) return f(Shape<0, 2, 256>());
+  if (vec && gs <= 6144) return f(Shape<0, 2, 384>());
   if (gs <= 8192) return f(Shape<0, 2>());
   return f(Shape<0, 4>());
 }

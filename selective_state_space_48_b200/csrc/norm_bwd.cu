@@ -35,6 +35,17 @@ template <typename T, typename R, int MODE, typename S> struct Ring {
   static constexpr bool kUsed = 16 * S::kMaxThreads * kPieces * kStages <= 200 * 1024;
 };
 
+// Blocks that an SM's registers hold.  Two pieces of a thread want 111
+// registers; where every tensor is bf16 three blocks of 256 threads at 80 are
+// faster than two (16384 rows of 4096: 129 us, 136; four at 64: 134), with fp32
+// residuals two (2560 channels: 136 us, 150 with three).
+template <typename T, typename R, typename S>
+constexpr int kResident = S::TPR ? 4
+                          : S::NV == 1 ? (sizeof(T) == 2 ? 2 : 1)
+                          : S::kMaxThreads == 256 ? (sizeof(R) == 2 ? 3 : 2)
+                          : S::kMaxThreads == 384 ? 2
+                                                  : 1;
+
 __device__ __forceinline__ float rcp_mufu(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -48,8 +59,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
 }
 
 template <typename T, typename R, int MODE, typename S, bool VEC>
-__global__ void __launch_bounds__(S::kMaxThreads,
-                                  S::TPR ? 4 : (S::NV == 1 && sizeof(T) == 2 ? 2 : 1))
+__global__ void __launch_bounds__(S::kMaxThreads, kResident<T, R, S>)
     norm_bwd_kernel(const Params p) {
   constexpr int NV = S::NV;
   using Rg = Ring<T, R, MODE, S>;
@@ -298,13 +308,14 @@ __global__ void __launch_bounds__(512) line_sum_kernel(const float *pa, float *o
   }
 }
 
-// Row blocks of a backward call: as many in all as fit the SMs at once, by
+// Row blocks of a backward call: as many in all as are on the SMs at once, by
 // their threads and their shared memory (of blocks of 128 threads with several
-// rows, 6 were best of 4 .. 16; rows that are not vectors leave longer lines of
-// scalars: 512 threads of an SM took 27 us for 4096 rows of 1155, 1024 took 33).
+// rows, 6 were best of 4 .. 16; rows that are not vectors are better off with
+// fewer lines: 1000 rows of 1155 in fp32 took 12.6 us with 512 threads to an
+// SM, 15.3 with 1024).
 template <typename S>
-int64_t row_blocks(int64_t rows, int64_t ng, int64_t gs, bool vec, int ring, int sms) {
-  int per = S::TPR ? 6 : std::min(8, (vec ? 1024 : 512) / S::threads(gs));
+int64_t row_blocks(int64_t rows, int64_t ng, int64_t gs, int sm_threads, int ring, int sms) {
+  int per = S::TPR ? 6 : std::min(8, sm_threads / S::threads(gs));
   per = std::max(1, std::min(per, ring > 0 ? 220 * 1024 / (ring + 1024) : per));
   const int64_t want = std::max<int64_t>(1, sms * per / ng);
   return std::min<int64_t>(want, (rows + S::kRows - 1) / S::kRows);
@@ -318,12 +329,11 @@ mss_status sm_count(int *sms) {
   return MSS_OK;
 }
 
-// floats that one set of partial sums takes at most (rows of scalars have no
-// more blocks than vectors of the same length)
+// floats that one set of partial sums takes at most, whatever the types
 int64_t part_floats(int64_t rows, int64_t ng, int64_t gs, int sms) {
   return by_shape(gs, true, [&](auto s) {
     using S = decltype(s);
-    return row_blocks<S>(rows, ng, gs, true, 0, sms) * kLines<S> * ng * gs;
+    return row_blocks<S>(rows, ng, gs, 1024, 0, sms) * kLines<S> * ng * gs;
   });
 }
 
@@ -334,9 +344,13 @@ cudaError_t launch(const Params &p, bool vec, int sms, float *dw, float *ds, cud
     const int threads = S::threads(p.gs);
     using Rg = Ring<T, R, MODE, S>;
     const int smem = vec && Rg::kUsed ? threads * 16 * Rg::kPieces * Rg::kStages : 0;
-    const int64_t rb = row_blocks<S>(p.rows, p.ng, p.gs, vec, smem, sms);
+    const int sm_threads = !vec ? 512 : S::kVector ? S::kMaxThreads * kResident<T, R, S> : 1024;
+    const int64_t rb = row_blocks<S>(p.rows, p.ng, p.gs, sm_threads, smem, sms);
     const dim3 grid(static_cast<unsigned>(rb), static_cast<unsigned>(p.ng));
-    auto kernel = vec ? norm_bwd_kernel<T, R, MODE, S, true> : norm_bwd_kernel<T, R, MODE, S, false>;
+    auto kernel = norm_bwd_kernel<T, R, MODE, S, true>;
+    if constexpr (!S::kVector) {
+      if (!vec) kernel = norm_bwd_kernel<T, R, MODE, S, false>;
+    }
     if (smem > 40 * 1024) {  // (48 KB with the static part) per launch: the current device's
       const cudaError_t a =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

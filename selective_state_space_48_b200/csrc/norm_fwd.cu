@@ -82,10 +82,11 @@ cudaError_t launch(const Params &p, bool vec, cudaStream_t stream) {
     using S = decltype(shape);
     const unsigned grid = static_cast<unsigned>((p.rows * p.ng + S::kRows - 1) / S::kRows);
     const int threads = S::threads(p.gs);
-    if (vec)
-      norm_fwd_kernel<T, R, MODE, S, true><<<grid, threads, 0, stream>>>(p);
-    else
-      norm_fwd_kernel<T, R, MODE, S, false><<<grid, threads, 0, stream>>>(p);
+    auto kernel = norm_fwd_kernel<T, R, MODE, S, true>;
+    if constexpr (!S::kVector) {
+      if (!vec) kernel = norm_fwd_kernel<T, R, MODE, S, false>;
+    }
+    kernel<<<grid, threads, 0, stream>>>(p);
     return cudaGetLastError();
   });
 }
