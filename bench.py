@@ -138,7 +138,7 @@ KERNEL_SOURCES = {
     "fwd": ("device_math.cuh", "scan_fwd.cu", "scan_fwd.cuh"),
     "bwd": ("device_math.cuh", "scan_bwd.cu", "scan_bwd.cuh"),
     "decode": ("device_math.cuh", "state_update.cu"),
-    "ssd": ("device_math.cuh", "ssd_fwd.cu"),
+    "ssd": ("device_math.cuh", "ssd_fwd.cu", "tcgen05.cuh"),
 }
 
 

@@ -3,8 +3,8 @@
 //   u_t = b_t (v_t - a_t S k_t),  S <- a_t S + u_t k_t^T,  y_t = scale S q_t
 //
 // Eight lanes share a row of S (headdim x dstate) and hold its columns in
-// registers, four neighbouring columns of every 32; a thread holds RPT rows.
-// Both readouts are taken from the state before the step,
+// registers, four neighbouring columns of every 32; a thread holds one row or
+// two.  Both readouts are taken from the state before the step,
 //
 //   S_t q = a S_{t-1} q + u (k . q),
 //
@@ -13,7 +13,7 @@
 //
 // One token (the decode step) is bound by reading and writing the fp32 state
 // (8 headdim dstate bytes per head), every load of which is issued before the
-// arithmetic: 192 sequences of 32 heads of 128 x 128 take 134 us, 92 % of the
+// arithmetic: 192 sequences of 32 heads of 128 x 128 take 127 us, 97 % of the
 // copy bandwidth.
 //
 // Over more steps the chain of a step (dots, three shuffles, update) bounds it.
@@ -22,7 +22,7 @@
 // put into shared memory as fp32, where the gates and k . q of its steps are
 // taken by one thread or eight lanes each.  (Loading one step ahead into
 // registers left a step waiting for memory: 227 us for 2 x 517 steps of 6
-// heads of 64 x 64 in fp32, 89 us this way.)
+// heads of 64 x 64 in fp32, 90 us this way.)
 #include "gated_delta.cuh"
 
 #include <cuda_bf16.h>
@@ -41,7 +41,6 @@ constexpr int kThreads = 128;
 // of one sequence 8.0 / 16.7 at 16 steps, 13.5 / 16.3 at 32, 24 / 16 at 64; of
 // 8 sequences 24 / 33, 42 / 32, 79 / 33; of 32 86 / 119, 156 / 118, 300 / 127.
 constexpr int64_t kChunkSteps = 32;
-constexpr int kGroups = kThreads / 8;  // rows of a block side by side
 
 // Four columns from `col` of a row of n columns: one vector load where VEC,
 // else element by element with zeros past the end.
@@ -60,24 +59,34 @@ __device__ __forceinline__ float4 row4(const T *row, int col, int n) {
 __device__ __forceinline__ float dot4(float4 a, float4 b, float s) {
   return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, s))));
 }
-__device__ __forceinline__ float sum8(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 1);
-  v += __shfl_xor_sync(0xffffffffu, v, 2);
-  return v + __shfl_xor_sync(0xffffffffu, v, 4);
+template <int LANES> __device__ __forceinline__ float sum_lanes(float v) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
+
+// How rows of the state lie on a block: LANES threads share a row and hold NV
+// vectors of four columns each, LANES vectors apart; a thread holds RPT rows,
+// kSide apart.
+template <int LANES_, int NV_, int RPT_> struct Layout {
+  static constexpr int LANES = LANES_, NV = NV_, RPT = RPT_;
+  static constexpr int kSide = kThreads / LANES, kRows = kSide * RPT;  // of a block
+  static constexpr int kCols = 4 * LANES * NV;
+  static __device__ __forceinline__ int column(int c, int lane) { return 4 * (c * LANES + lane); }
+};
 
 // the thread's part of the state at `src` (NULL: zeros).  It is read once and
 // written once: streaming accesses keep it from displacing the other inputs in
 // the caches.
-template <int NV, int RPT, bool VEC>
-__device__ __forceinline__ void load_state(float4 (&S)[RPT][NV], const float *src, int row0, int P,
-                                           int N, int lane8) {
+template <typename Y, bool VEC>
+__device__ __forceinline__ void load_state(float4 (&S)[Y::RPT][Y::NV], const float *src, int row0,
+                                           int P, int N, int lane) {
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    const int row = row0 + r * kGroups;
+  for (int r = 0; r < Y::RPT; ++r) {
+    const int row = row0 + r * Y::kSide;
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      const int col = c * 32 + lane8 * 4;
+    for (int c = 0; c < Y::NV; ++c) {
+      const int col = Y::column(c, lane);
       S[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (src && row < P) {
         const float *at = src + static_cast<int64_t>(row) * N;
@@ -90,18 +99,18 @@ __device__ __forceinline__ void load_state(float4 (&S)[RPT][NV], const float *sr
     }
   }
 }
-template <int NV, int RPT, bool VEC>
-__device__ __forceinline__ void store_state(const float4 (&S)[RPT][NV], float *dst, int row0, int P,
-                                            int N, int lane8) {
+template <typename Y, bool VEC>
+__device__ __forceinline__ void store_state(const float4 (&S)[Y::RPT][Y::NV], float *dst, int row0,
+                                            int P, int N, int lane) {
   if (!dst) return;
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    const int row = row0 + r * kGroups;
+  for (int r = 0; r < Y::RPT; ++r) {
+    const int row = row0 + r * Y::kSide;
     if (row >= P) continue;
     float *at = dst + static_cast<int64_t>(row) * N;
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      const int col = c * 32 + lane8 * 4;
+    for (int c = 0; c < Y::NV; ++c) {
+      const int col = Y::column(c, lane);
       if constexpr (VEC) {
         if (col < N) __stcs(reinterpret_cast<float4 *>(at + col), S[r][c]);
       } else {
@@ -114,31 +123,34 @@ __device__ __forceinline__ void store_state(const float4 (&S)[RPT][NV], float *d
   }
 }
 
-// k . q, and S k and S q of the thread's rows, over the eight lanes of each
-template <int NV>
+// k . q, and S k and S q of the thread's rows, over the lanes of each
+template <int LANES, int NV>
 __device__ __forceinline__ float inner(const float4 (&k)[NV], const float4 (&q)[NV]) {
   float s = 0.f;
 #pragma unroll
   for (int c = 0; c < NV; ++c) s = dot4(k[c], q[c], s);
-  return sum8(s);
+  return sum_lanes<LANES>(s);
 }
-template <int NV, int RPT>
-__device__ __forceinline__ void readouts(const float4 (&S)[RPT][NV], const float4 (&k)[NV],
-                                         const float4 (&q)[NV], float (&sk)[RPT],
-                                         float (&sq)[RPT]) {
+template <typename Y>
+__device__ __forceinline__ void readouts(const float4 (&S)[Y::RPT][Y::NV],
+                                         const float4 (&k)[Y::NV], const float4 (&q)[Y::NV],
+                                         float (&sk)[Y::RPT], float (&sq)[Y::RPT]) {
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    sk[r] = sq[r] = 0.f;
+  for (int r = 0; r < Y::RPT; ++r) {
+    // (two sums of each: half the chain)
+    float a[2] = {0.f, 0.f}, b[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      sk[r] = dot4(S[r][c], k[c], sk[r]);
-      sq[r] = dot4(S[r][c], q[c], sq[r]);
+    for (int c = 0; c < Y::NV; ++c) {
+      a[c & 1] = dot4(S[r][c], k[c], a[c & 1]);
+      b[c & 1] = dot4(S[r][c], q[c], b[c & 1]);
     }
+    sk[r] = a[0] + a[1];
+    sq[r] = b[0] + b[1];
   }
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-    sk[r] = sum8(sk[r]);
-    sq[r] = sum8(sq[r]);
+  for (int r = 0; r < Y::RPT; ++r) {
+    sk[r] = sum_lanes<Y::LANES>(sk[r]);
+    sq[r] = sum_lanes<Y::LANES>(sq[r]);
   }
 }
 // S <- a S + u k
@@ -155,21 +167,21 @@ __device__ __forceinline__ void write_row(float4 (&S)[NV], const float4 (&k)[NV]
 }
 
 // the place of a thread and the tensors of its sequence and head
-template <typename InT, typename OutT, int RPT> struct Seat {
-  int h, lane8, row0;
+template <typename InT, typename OutT, typename Y> struct Seat {
+  int h, lane, row0;
   int64_t base, t0, t1;
   float A2, bias;
   const InT *q, *k, *v, *dt, *beta;
   OutT *y;
   __device__ __forceinline__ explicit Seat(const DeltaParams &p) {
-    const int nrb = static_cast<int>((p.P + kGroups * RPT - 1) / (kGroups * RPT));
+    const int nrb = static_cast<int>((p.P + Y::kRows - 1) / Y::kRows);
     const int64_t sh = blockIdx.x / nrb;
     const int rb = static_cast<int>(blockIdx.x - sh * nrb);
     const int64_t s = sh / p.H;
     h = static_cast<int>(sh - s * p.H);
     const int g = h / static_cast<int>(p.H / p.G);
-    lane8 = threadIdx.x & 7;
-    row0 = rb * kGroups * RPT + (threadIdx.x >> 3);
+    lane = threadIdx.x % Y::LANES;
+    row0 = rb * Y::kRows + threadIdx.x / Y::LANES;
     base = sh * p.P * p.N;
     int64_t b;
     delta_span(p, s, b, t0, t1);
@@ -185,46 +197,47 @@ template <typename InT, typename OutT, int RPT> struct Seat {
 };
 
 // one token of every sequence (not packed)
-template <typename InT, typename OutT, int NV, int RPT, bool VEC>
+template <typename InT, typename OutT, typename Y, bool VEC>
 __global__ void __launch_bounds__(kThreads) delta_token_kernel(const DeltaParams p) {
+  constexpr int NV = Y::NV, RPT = Y::RPT;
   const int N = static_cast<int>(p.N), P = static_cast<int>(p.P);
-  const Seat<InT, OutT, RPT> at(p);
+  const Seat<InT, OutT, Y> at(p);
   float4 S[RPT][NV], k[NV], q[NV];
-  load_state<NV, RPT, VEC>(S, p.h0 ? p.h0 + at.base : nullptr, at.row0, P, N, at.lane8);
+  load_state<Y, VEC>(S, p.h0 ? p.h0 + at.base : nullptr, at.row0, P, N, at.lane);
   float v[RPT], sk[RPT], sq[RPT], g2, beta;
 #pragma unroll
   for (int c = 0; c < NV; ++c) {
-    k[c] = row4<InT, VEC>(at.k, c * 32 + at.lane8 * 4, N);
-    q[c] = row4<InT, VEC>(at.q, c * 32 + at.lane8 * 4, N);
+    k[c] = row4<InT, VEC>(at.k, Y::column(c, at.lane), N);
+    q[c] = row4<InT, VEC>(at.q, Y::column(c, at.lane), N);
   }
 #pragma unroll
   for (int r = 0; r < RPT; ++r)
-    v[r] = at.row0 + r * kGroups < P ? to_f32<InT>(at.v[at.row0 + r * kGroups]) : 0.f;
+    v[r] = at.row0 + r * Y::kSide < P ? to_f32<InT>(at.v[at.row0 + r * Y::kSide]) : 0.f;
   delta_gates<InT>(p, to_f32<InT>(*at.dt), to_f32<InT>(*at.beta), at.A2, at.bias, g2, beta);
-  const float a = ex2_mufu(g2), kq = inner<NV>(k, q);
-  readouts<NV, RPT>(S, k, q, sk, sq);
+  const float a = ex2_mufu(g2), kq = inner<Y::LANES>(k, q);
+  readouts<Y>(S, k, q, sk, sq);
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     const float u = beta * (v[r] - a * sk[r]);
     write_row<NV>(S[r], k, a, u);
-    const int row = at.row0 + r * kGroups;
-    if (at.lane8 == 0 && row < P) at.y[row] = from_f32<OutT>(p.scale * fmaf(a, sq[r], u * kq));
+    const int row = at.row0 + r * Y::kSide;
+    if (at.lane == 0 && row < P) at.y[row] = from_f32<OutT>(p.scale * fmaf(a, sq[r], u * kq));
   }
-  store_state<NV, RPT, VEC>(S, p.last ? p.last + at.base : nullptr, at.row0, P, N, at.lane8);
+  store_state<Y, VEC>(S, p.last ? p.last + at.base : nullptr, at.row0, P, N, at.lane);
 }
 
 // sequences of any length
-template <typename InT, typename OutT, int NV, int RPT, bool VEC>
+template <typename InT, typename OutT, typename Y, bool VEC>
 __global__ void __launch_bounds__(kThreads) delta_steps_kernel(const DeltaParams p) {
-  constexpr int TB = NV == 8 ? 8 : 16;              // steps of a tile
-  constexpr int kItems = TB * NV * 8 / kThreads;    // of four columns, per thread, of q and of k
-  constexpr int kRows = kGroups * RPT, kVals = TB * kRows / kThreads;
-  __shared__ __align__(16) float ks[2][TB][NV * 32], qs[2][TB][NV * 32];
-  __shared__ float vs[2][TB][kRows];
-  __shared__ __align__(16) float gate[2][TB][4];  // a, b, k . q
+  constexpr int NV = Y::NV, RPT = Y::RPT, kCols = Y::kCols, kRows = Y::kRows;
+  constexpr int TB = kCols == 256 ? 8 : 16;                       // steps of a tile
+  constexpr int kItems = TB * kCols / 4 / kThreads;               // vectors of a thread, of q and of k
+  constexpr int kVals = TB * kRows / kThreads;
+  __shared__ __align__(16) float ks[2][TB][kCols], qs[2][TB][kCols];
+  __shared__ float vs[2][TB][kRows], gate[2][TB][4];  // gate: a, b, k . q
   const int N = static_cast<int>(p.N), P = static_cast<int>(p.P), tid = threadIdx.x;
-  const Seat<InT, OutT, RPT> at(p);
-  const int block0 = at.row0 - (tid >> 3);
+  const Seat<InT, OutT, Y> at(p);
+  const int side = tid / Y::LANES, block0 = at.row0 - side;
 
   float4 kn[kItems], qn[kItems];
   float vn[kVals], dtn = 0.f, bn = 0.f;
@@ -232,8 +245,8 @@ __global__ void __launch_bounds__(kThreads) delta_steps_kernel(const DeltaParams
   auto load = [&](int64_t t) {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
-      const int item = tid + i * kThreads, col = item % (NV * 8) * 4;
-      const int64_t r = t + item / (NV * 8);
+      const int item = tid + i * kThreads, col = item % (kCols / 4) * 4;
+      const int64_t r = t + item / (kCols / 4);
       const bool in = r < at.t1;
       kn[i] = row4<InT, VEC>(at.k + (in ? r * p.sk[1] : 0), col, in ? N : 0);
       qn[i] = row4<InT, VEC>(at.q + (in ? r * p.sq[1] : 0), col, in ? N : 0);
@@ -266,22 +279,23 @@ __global__ void __launch_bounds__(kThreads) delta_steps_kernel(const DeltaParams
       gate[buf][tid][1] = b;
     }
     __syncthreads();
-    if ((tid >> 3) < TB) {  // whole warps
-      float4 k[NV], q[NV];
+    if ((tid >> 3) < TB) {  // k . q, eight lanes to a step (whole warps)
+      constexpr int n = kCols / 32;
+      float4 k[n], q[n];
 #pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        k[c] = *reinterpret_cast<const float4 *>(&ks[buf][tid >> 3][c * 32 + at.lane8 * 4]);
-        q[c] = *reinterpret_cast<const float4 *>(&qs[buf][tid >> 3][c * 32 + at.lane8 * 4]);
+      for (int c = 0; c < n; ++c) {
+        k[c] = *reinterpret_cast<const float4 *>(&ks[buf][tid >> 3][32 * c + 4 * (tid & 7)]);
+        q[c] = *reinterpret_cast<const float4 *>(&qs[buf][tid >> 3][32 * c + 4 * (tid & 7)]);
       }
-      const float kq = inner<NV>(k, q);
-      if (at.lane8 == 0) gate[buf][tid >> 3][2] = kq;
+      const float kq = inner<8>(k, q);
+      if ((tid & 7) == 0) gate[buf][tid >> 3][2] = kq;
     }
     __syncthreads();
   };
 
   if (at.t0 < at.t1) load(at.t0);
   float4 S[RPT][NV];
-  load_state<NV, RPT, VEC>(S, p.h0 ? p.h0 + at.base : nullptr, at.row0, P, N, at.lane8);
+  load_state<Y, VEC>(S, p.h0 ? p.h0 + at.base : nullptr, at.row0, P, N, at.lane);
   if (at.t0 < at.t1) put(0);
   int buf = 0;
   for (int64_t t = at.t0; t < at.t1; t += TB, buf ^= 1) {
@@ -293,18 +307,18 @@ __global__ void __launch_bounds__(kThreads) delta_steps_kernel(const DeltaParams
       float4 k[NV], q[NV];
 #pragma unroll
       for (int c = 0; c < NV; ++c) {
-        k[c] = *reinterpret_cast<const float4 *>(&ks[buf][j][c * 32 + at.lane8 * 4]);
-        q[c] = *reinterpret_cast<const float4 *>(&qs[buf][j][c * 32 + at.lane8 * 4]);
+        k[c] = *reinterpret_cast<const float4 *>(&ks[buf][j][Y::column(c, at.lane)]);
+        q[c] = *reinterpret_cast<const float4 *>(&qs[buf][j][Y::column(c, at.lane)]);
       }
       const float a = gate[buf][j][0], beta = gate[buf][j][1], kq = gate[buf][j][2];
       float sk[RPT], sq[RPT];
-      readouts<NV, RPT>(S, k, q, sk, sq);
+      readouts<Y>(S, k, q, sk, sq);
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
-        const float u = beta * (vs[buf][j][(tid >> 3) + r * kGroups] - a * sk[r]);
+        const float u = beta * (vs[buf][j][side + r * Y::kSide] - a * sk[r]);
         write_row<NV>(S[r], k, a, u);
-        const int row = at.row0 + r * kGroups;
-        if (at.lane8 == 0 && row < P)
+        const int row = at.row0 + r * Y::kSide;
+        if (at.lane == 0 && row < P)
           yp[j * p.sy[1] + row] = from_f32<OutT>(p.scale * fmaf(a, sq[r], u * kq));
       }
     }
@@ -312,30 +326,33 @@ __global__ void __launch_bounds__(kThreads) delta_steps_kernel(const DeltaParams
     // the ones of the last tile)
     if (t + TB < at.t1) put(buf ^ 1);
   }
-  store_state<NV, RPT, VEC>(S, p.last ? p.last + at.base : nullptr, at.row0, P, N, at.lane8);
+  store_state<Y, VEC>(S, p.last ? p.last + at.base : nullptr, at.row0, P, N, at.lane);
 }
 
 bool al(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-template <typename InT, typename OutT, int NV, int RPT, bool VEC>
-cudaError_t go(const DeltaParams &p, cudaStream_t stream) {
-  const int64_t nrb = (p.P + kGroups * RPT - 1) / (kGroups * RPT);
-  const unsigned grid = static_cast<unsigned>(p.seqs * p.H * nrb);
-  if (p.L == 1 && !p.cu)
-    delta_token_kernel<InT, OutT, NV, RPT, VEC><<<grid, kThreads, 0, stream>>>(p);
-  else
-    delta_steps_kernel<InT, OutT, NV, RPT, VEC><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+template <typename Y> unsigned blocks(const DeltaParams &p) {
+  return static_cast<unsigned>(p.seqs * p.H * ((p.P + Y::kRows - 1) / Y::kRows));
 }
 
-// Two rows of a thread share its k and q (one row in twice the blocks: 8
-// sequences of 64 steps of 32 heads of 128 x 128, 111 us against 84; it is 5 %
-// faster where there are few blocks); at dstate 256 two would not fit.
+// Eight lanes read 128 bytes of a row of the state at a time.  Two rows of a
+// thread share its k and q (steps, 8 sequences of 64 of 32 heads of 128 x 128:
+// 80 us, 111 with one row in twice the blocks, 107 with four lanes to a row; few
+// blocks gain 5 % from one row); at dstate 256 two would not fit.
 template <typename InT, typename OutT, bool VEC>
 cudaError_t by_size(const DeltaParams &p, cudaStream_t stream) {
-  if (p.N <= 64) return go<InT, OutT, 2, 2, VEC>(p, stream);
-  if (p.N <= 128) return go<InT, OutT, 4, 2, VEC>(p, stream);
-  return go<InT, OutT, 8, 1, VEC>(p, stream);
+  const bool token = p.L == 1 && !p.cu;
+  auto go = [&](auto layout) {
+    using Y = decltype(layout);
+    if (token)
+      delta_token_kernel<InT, OutT, Y, VEC><<<blocks<Y>(p), kThreads, 0, stream>>>(p);
+    else
+      delta_steps_kernel<InT, OutT, Y, VEC><<<blocks<Y>(p), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+  };
+  if (p.N <= 64) return go(Layout<8, 2, 2>());
+  if (p.N <= 128) return go(Layout<8, 4, 2>());
+  return go(Layout<8, 8, 1>());
 }
 
 // four-column vectors everywhere: the state's rows and the q, k rows
@@ -378,7 +395,7 @@ mss_status check_sizes(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t G
   // sizes whose grid, 32-bit tensor coordinates or row index would overflow
   const int64_t lim = int64_t(1) << 30;
   if (P > lim || H > lim || L > lim || batch > lim || batch > lim / H ||
-      batch * H > lim / ((P + kGroups - 1) / kGroups))
+      batch * H > lim / ((P + 15) / 16))
     return MSS_ERR_UNSUPPORTED;
   return MSS_OK;
 }
