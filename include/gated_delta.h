@@ -30,7 +30,10 @@
  *              and then Y = diag(e^c) Q H0^T + (Q K^T o e^(c_t - c_s)) U and
  *              S = e^(c_last) H0 + U^T diag(e^(c_last - c)) K.  Operands that
  *              are not bf16 already enter the products as the sum of two
- *              bf16 values, so the result keeps about 16 bits.
+ *              bf16 values, so the result keeps about 16 bits.  With a
+ *              workspace, long sequences of few heads are cut into segments
+ *              that run beside each other: the state passes a segment as
+ *              S_end = S_start M + B, with M and B from a first pass.
  * A NaN or an infinity in a step's inputs spoils that head from the step on
  * (recurrent) or from the first step of its chunk on (chunked), nothing else.
  *
@@ -108,10 +111,18 @@ typedef struct mss_delta_args {
   int64_t num_seqs;
   int plan;
   uint64_t spin_timeout_ns;
+  void *workspace;      /* optional; 16-byte aligned */
+  size_t workspace_bytes;
 } mss_delta_args;
 
 /* Forward over whole sequences: y (and last_state). */
 mss_status gated_delta_fwd(const mss_delta_args *args, void *stream);
+
+/* Bytes of workspace with which the chunked evaluation cuts long sequences of
+ * few heads into segments that run beside each other (0: these sizes gain
+ * nothing on the current device).  Without a workspace every sequence runs
+ * whole; one that is too small is MSS_ERR_WORKSPACE. */
+mss_status mss_gated_delta_workspace_size(const mss_delta_args *args, size_t *bytes);
 
 typedef struct mss_delta_update_args {
   int64_t batch;

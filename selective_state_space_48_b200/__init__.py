@@ -67,6 +67,7 @@ EXPORTED_SYMBOLS = (
     "gated_delta_fwd",
     "gated_delta_update",
     "mss_gated_delta_status",
+    "mss_gated_delta_workspace_size",
     "gated_rmsnorm_fwd",
     "gated_rmsnorm_bwd",
     "mss_gated_rmsnorm_bwd_workspace_size",
@@ -194,6 +195,8 @@ class DeltaArgs(ctypes.Structure):
         ("num_seqs", ctypes.c_int64),
         ("plan", ctypes.c_int),
         ("spin_timeout_ns", ctypes.c_uint64),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -287,7 +290,8 @@ def _bind(lib):
         getattr(lib, name).restype = ctypes.c_int
     lib.mss_gated_delta_status.argtypes = [ctypes.c_void_p]
     lib.mss_gated_delta_status.restype = ctypes.c_int
-    for name, args in (("mss_gated_rmsnorm_bwd_workspace_size", GatedNormArgs),
+    for name, args in (("mss_gated_delta_workspace_size", DeltaArgs),
+                       ("mss_gated_rmsnorm_bwd_workspace_size", GatedNormArgs),
                        ("mss_add_rmsnorm_bwd_workspace_size", AddNormArgs)):
         getattr(lib, name).argtypes = [P(args), P(ctypes.c_size_t)]
         getattr(lib, name).restype = ctypes.c_int
@@ -878,7 +882,7 @@ def _same(t, dtype, device, shape):
 
 
 def _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y,
-                  last_state, cu_seqlens, plan, spin_timeout_ns):
+                  last_state, cu_seqlens, plan, spin_timeout_ns, workspace):
     """The values of ``mss_delta_args`` in order, after the checks."""
     if not isinstance(v, torch.Tensor) or not isinstance(q, torch.Tensor):
         raise TypeError("q and v must be CUDA tensors")
@@ -918,7 +922,30 @@ def _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scal
         0 if y is None else y.data_ptr(), 0 if last_state is None else last_state.data_ptr(),
         *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *dt.stride(), *beta.stride(),
         *((0, 0, 0) if y is None else y.stride()[:3]), cu, seqs if cu else 0, int(plan),
-        int(spin_timeout_ns))
+        int(spin_timeout_ns), *workspace)
+
+
+def _workspace(nbytes, device, stream):
+    """The workspace of a call; on the caller's own stream it is kept
+    until that stream has used it (on the current one the allocator does)."""
+    if not nbytes:
+        return None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws, ws.data_ptr()
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_workspace_bytes(batch, seqlen, nheads, headdim, dstate, device_index):
+    """Workspace bytes of a chunked call of these sizes on this device (0
+    also for sizes that the call itself refuses)."""
+    a, n = DeltaArgs(), ctypes.c_size_t(0)
+    a.batch, a.seqlen, a.nheads, a.headdim, a.ngroups = batch, seqlen, nheads, headdim, 1
+    a.dstate, a.in_dtype = dstate, MSS_BF16
+    with torch.cuda.device(device_index):
+        load_library().mss_gated_delta_workspace_size(ctypes.byref(a), ctypes.byref(n))
+    return int(n.value)
 
 
 _pack_delta = _packer(DeltaArgs)
@@ -926,10 +953,14 @@ _pack_delta = _packer(DeltaArgs)
 
 def make_gated_delta_args(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True,
                           beta_sigmoid=True, scale=None, h0=None, y=None, last_state=None,
-                          cu_seqlens=None, plan=MSS_DELTA_AUTO, spin_timeout_ns=0) -> DeltaArgs:
+                          cu_seqlens=None, plan=MSS_DELTA_AUTO, spin_timeout_ns=0,
+                          workspace=None) -> DeltaArgs:
+    if workspace is not None:
+        _check_views(q.device, [("workspace", workspace, torch.uint8, None, "dense")])
     return DeltaArgs.from_buffer_copy(_pack_delta(*_delta_values(
         q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y, last_state,
-        cu_seqlens, plan, spin_timeout_ns)))
+        cu_seqlens, plan, spin_timeout_ns,
+        (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel()))))
 
 
 def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_sigmoid=True,
@@ -957,9 +988,16 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
         seqs = v.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
         last_state = torch.empty((seqs, v.shape[2], v.shape[3], q.shape[-1]),
                                  dtype=torch.float32, device=v.device)
+    ws, room = None, (0, 0)
+    if cu_seqlens is None and v.dtype is torch.bfloat16 and v.is_cuda and \
+            plan != MSS_DELTA_RECURRENT:
+        nbytes = _delta_workspace_bytes(*v.shape, q.shape[-1], v.device.index)
+        if nbytes:
+            ws, pws = _workspace(nbytes, v.device, stream)
+            room = (pws, nbytes)
     _enqueue("gated_delta_fwd", _pack_delta(*_delta_values(
         q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y, last_state,
-        cu_seqlens, plan, 0)), q.device, stream)
+        cu_seqlens, plan, 0, room)), q.device, stream)
     if check_status:
         with _on_device(q.device, stream) as s:
             rc = load_library().mss_gated_delta_status(_stream_handle(s))
@@ -1073,17 +1111,6 @@ def _norm_workspace_bytes(name, rows, width, group, sums, device_index):
     return int(n.value)
 
 
-def _norm_workspace(nbytes, device, stream):
-    """The workspace of a backward call; on the caller's own stream it is kept
-    until that stream has used it (on the current one the allocator does)."""
-    if not nbytes:
-        return None, 0
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws, ws.data_ptr()
-
-
 def _gated_norm_sizes(x, weight, group_size):
     """rows, width, group size, and whether the groups share the weight."""
     if not isinstance(x, torch.Tensor) or x.dim() < 1:
@@ -1138,7 +1165,7 @@ def gated_rmsnorm_bwd(x, z, weight, dy, eps=1e-5, group_size=None, norm_before_g
     (px, pz, pdy, pdx, pdz), (sx, sz, sdy, sdx, sdz) = _norm_rows(dev, shape, (
         ("x", x, kind), ("z", z, kind), ("dy", dy, kind), ("dx", dx, kind), ("dz", dz, kind)))
     nbytes = _norm_workspace_bytes("gated", rows, width, gs, 1, dev.index) if need_dweight else 0
-    ws, pws = _norm_workspace(nbytes, dev, stream)
+    ws, pws = _workspace(nbytes, dev, stream)
     _enqueue("gated_rmsnorm_bwd", _pack_gated_norm(
         rows, width, gs, _dtype_code(kind), bool(norm_before_gate), shared, eps, px, pz,
         weight.data_ptr(), 0, pdy, pdx, pdz, dw.data_ptr() if need_dweight else 0, sx, sz, 0, sdy,
@@ -1210,7 +1237,7 @@ def add_rmsnorm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, scale=
         ("x", x if need_dscale else None, kind), ("dx", dx, kind), ("dresidual", dres, rd)))
     sums = (1 if need_dweight else 0) + (2 if need_dscale else 0)
     nbytes = _norm_workspace_bytes("add", rows, width, 0, sums, dev.index) if sums else 0
-    ws, pws = _norm_workspace(nbytes, dev, stream)
+    ws, pws = _workspace(nbytes, dev, stream)
     _enqueue("add_rmsnorm_bwd", _pack_add_norm(
         rows, width, _dtype_code(kind), _dtype_code(rd), eps, px, 0,
         0 if scale is None else scale.data_ptr(), weight.data_ptr(), 0, po, pdy, pdo, pdx, pdr,

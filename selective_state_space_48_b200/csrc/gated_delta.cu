@@ -400,6 +400,15 @@ mss_status check_sizes(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t G
   return MSS_OK;
 }
 
+// The cut of the call's sequences on the current device: p.segs, p.seg_chunks.
+mss_status segments(DeltaParams &p, int64_t *floats) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MSS_ERR_CUDA;
+  p.segs = delta_segments(p, sms, &p.seg_chunks, floats);
+  return MSS_OK;
+}
 
 }  // namespace
 
@@ -481,6 +490,15 @@ extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
                   (a->plan == MSS_DELTA_AUTO && p.L / (packed ? seqs : 1) >= kChunkSteps))) {
     p.status = delta_status_word();
     if (!p.status) return MSS_ERR_CUDA;
+    if (a->workspace && !packed) {
+      int64_t floats = 0;
+      const mss_status w = segments(p, &floats);
+      if (w != MSS_OK) return w;
+      if (!al(a->workspace, 16)) return MSS_ERR_INVALID_ARG;
+      if (a->workspace_bytes < static_cast<size_t>(floats) * 4) return MSS_ERR_WORKSPACE;
+      p.ends = static_cast<float *>(a->workspace);
+      p.moves = p.ends + (p.segs - 1) * p.seqs * p.H * p.P * p.N;
+    }
     return launch_delta_chunk(p, a->out_dtype == MSS_BF16, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? MSS_OK
@@ -490,6 +508,27 @@ extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MSS_OK
              : MSS_ERR_CUDA;
+}
+
+extern "C" mss_status mss_gated_delta_workspace_size(const mss_delta_args *a, size_t *bytes) {
+  if (!a || !bytes) return MSS_ERR_INVALID_ARG;
+  mss_status st = check_sizes(a->cu_seqlens ? a->num_seqs : a->batch, a->seqlen, a->nheads,
+                              a->headdim, a->ngroups, a->dstate, a->in_dtype, a->out_dtype);
+  if (st != MSS_OK) return st;
+  *bytes = 0;
+  if (a->cu_seqlens || a->in_dtype != MSS_BF16 || a->dstate > 128 ||
+      a->plan == MSS_DELTA_RECURRENT)
+    return MSS_OK;
+  DeltaParams p{};
+  p.seqs = p.batch = a->batch;
+  p.L = a->seqlen;
+  p.H = a->nheads;
+  p.P = a->headdim;
+  p.N = a->dstate;
+  int64_t floats = 0;
+  if ((st = segments(p, &floats)) != MSS_OK) return st;
+  *bytes = static_cast<size_t>(floats) * 4;
+  return MSS_OK;
 }
 
 extern "C" mss_status gated_delta_update(const mss_delta_update_args *a, void *stream) {

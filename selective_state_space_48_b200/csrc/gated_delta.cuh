@@ -25,6 +25,10 @@ struct DeltaParams {
   const int32_t *cu;
   unsigned *status;
   uint64_t spin_ns;
+  // sequences cut into `segs` segments of seg_chunks chunks (segs 0: whole);
+  // pass 1 or 2 of the two that then run (gated_delta_chunk.cu)
+  int segs, seg_chunks, pass;
+  float *ends, *moves;  // (segs - 1) states, (segs - 2) transitions of every head
 };
 
 // Steps [t0, t1) of sequence s in batch row b.  Packed offsets come from the
@@ -57,6 +61,9 @@ cudaError_t launch_delta_recurrent(const DeltaParams &p, bool in_bf16, bool out_
 // true where the chunked kernel applies to these types, sizes and addresses
 bool delta_chunk_applies(const DeltaParams &p, bool in_bf16);
 cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t stream);
+// segments that sequences of these sizes are best cut into on `sms` SMs (0:
+// none), their length in chunks, and the floats of workspace that takes
+int delta_segments(const DeltaParams &p, int sms, int *seg_chunks, int64_t *floats);
 unsigned *delta_status_word();
 
 }  // namespace sss48

@@ -391,11 +391,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
-  const int slices = static_cast<int>((p.P + 127) / 128);
-  const int64_t sh = blockIdx.x / slices;
-  const int p0 = static_cast<int>(blockIdx.x - sh * slices) * 128;
+  // the sequence, head and 128 rows; of a cut sequence the segment, and in its
+  // first pass whether this block takes the transition's rows (`move`)
+  int slices = static_cast<int>((p.P + 127) / 128), seg = 0;
+  int64_t task = blockIdx.x;
+  bool move = false;
+  if (p.segs) {
+    const int64_t heads = p.seqs * p.H, of_rows = (p.segs - 1) * heads * slices;
+    move = task >= of_rows;
+    if (move) {
+      task -= of_rows;
+      slices = 1;
+    }
+    seg = static_cast<int>(task / (heads * slices));
+    task -= seg * heads * slices;
+    if (move || p.pass == 2) ++seg;
+  }
+  const int64_t sh = task / slices;
+  const int p0 = static_cast<int>(task - sh * slices) * 128;
   int64_t seq = sh / p.H;
   const int h = static_cast<int>(sh - seq * p.H);
+  const int N = static_cast<int>(p.N), P = static_cast<int>(move ? p.N : p.P);
+  const bool write_y = p.pass != 1 || seg == 0;
+  if (move) {  // no values
+    for (int k = tid; k < kStageV / 16; k += kThreads)
+      *reinterpret_cast<uint4 *>(sm + oV + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
+  }
   // Packed sequences are taken longest first (the n-th of the grid is the n-th
   // longest): a long one that starts among the last runs on alone.  24 of 0 to
   // 1362 steps: 222 us, 263 in their own order.
@@ -423,9 +445,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (*tmem_slot != 0) *abort = 1;
 
   const int g = h / static_cast<int>(p.H / p.G);
-  const int N = static_cast<int>(p.N), P = static_cast<int>(p.P);
   int64_t b64, t0, t1;
   delta_span(p, seq, b64, t0, t1);
+  const float *h0 = p.h0;
+  float *last = p.last;
+  if (p.segs) {
+    const int64_t states = p.seqs * p.H * p.P * p.N, len = static_cast<int64_t>(p.seg_chunks) * C;
+    t0 = seg * len;
+    t1 = t1 - t0 > len ? t0 + len : t1;
+    if (p.pass == 2) {
+      h0 = p.ends + (seg - 1) * states;
+      if (seg < p.segs - 1) last = nullptr;
+    } else {
+      if (seg > 0) h0 = nullptr;
+      last = move ? p.moves + (seg - 1) * p.seqs * p.H * p.N * p.N : p.ends + seg * states;
+    }
+  }
   const int b = static_cast<int>(b64);
   const int total = static_cast<int>(t1 - t0);
   const int nc = __shfl_sync(0xffffffffu, (total + C - 1) / C, 0);
@@ -457,7 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; i <= nc; ++i) {
         if (i > 0) sy.wait(kEmptyV, (i - 1) & 1);
         if (*abort) break;
-        if (i < nc) {
+        if (i < nc && move) {
+          mbar_arrive(bar + kFullV + (i & 1));
+        } else if (i < nc) {
           const int t = static_cast<int>(t0) + i * C;
           uint64_t *full = bar + kFullV + (i & 1);
           mbar_expect_tx(full, kStageV);
@@ -470,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         sy.wait(kReadyY, (i - 1) & 1);
         const int t = static_cast<int>(t0) + (i - 1) * C, a = (i - 1) % 3;
         const unsigned char *y = sm + oKQ + a * kStageKQ + kHalf;
-        if (!*abort) {
+        if (write_y && !*abort) {
           tma_store_4d(&maps.y, y, p0, h, t, b);
           if (p0 + 64 < P) tma_store_4d(&maps.y, y + 2 * kHalf, p0 + 64, h, t, b);
         }
@@ -673,18 +710,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, e = (warp - 4) >> 2;
     const int row = p0 + 32 * q + lane;
     const uint32_t tl = static_cast<uint32_t>(32 * q) << 16;
-    const int64_t base = ((seq * p.H + h) * p.P + row) * p.N + 32 * e;
+    const int64_t base = ((seq * p.H + h) * P + row) * p.N + 32 * e;
     OutT *yp = static_cast<OutT *>(p.y) + b * p.sy[0] + h * p.sy[2] + t0 * p.sy[1] + row;
     float H[32];
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (p.h0 && row < P && 32 * e + j < N)
-        v = __ldcs(reinterpret_cast<const float4 *>(p.h0 + base + j));
+      if (h0 && row < P && 32 * e + j < N)
+        v = __ldcs(reinterpret_cast<const float4 *>(h0 + base + j));
       H[j] = v.x;
       H[j + 1] = v.y;
       H[j + 2] = v.z;
       H[j + 3] = v.w;
+    }
+    if (move) {  // the transition: where the unit rows go
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (32 * e + j == row) H[j] = 1.f;
     }
     float gam = 1.0f;
     // H <- 2^(c_last) H + U'^T K of chunk i
@@ -738,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_async_smem();
         }
         warp_arrive(bar + kReadyY, lane);
-      } else if (row < P) {
+      } else if (write_y && row < P) {
         OutT *yr = yp + static_cast<int64_t>(i * C + 16 * e) * p.sy[1];
 #pragma unroll
         for (int j = 0; j < 16; ++j)
@@ -822,11 +864,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       warp_arrive(bar + kReadyO, lane);
     }
-    if (p.last && row < P) {
+    if (last && row < P) {
 #pragma unroll
       for (int j = 0; j < 32; j += 4)
         if (32 * e + j < N)
-          __stcs(reinterpret_cast<float4 *>(p.last + base + j),
+          __stcs(reinterpret_cast<float4 *>(last + base + j),
                  make_float4(H[j], H[j + 1], H[j + 2], H[j + 3]));
     }
   } else if (warp >= 20) {
@@ -979,6 +1021,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// The states that segments start from: ends[s] <- ends[s] + ends[s - 1] M_s, in
+// order, with ends[0] the state after the first segment and ends[s] on entry
+// what segment s makes of a zero state.  kJoinRows rows of a head's state to a
+// block, 2 rows of 4 columns to a thread; the next M is on its way into shared
+// memory meanwhile (read where it is used, M's latency made a segment 6 us).
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(256) delta_join_kernel(const DeltaParams p) {
+  extern __shared__ __align__(16) float ms[];  // one or two of M
+  __shared__ __align__(8) float rows[128][kJoinRows + 2];
+  const int N = static_cast<int>(p.N), c = 4 * (threadIdx.x & 31), r0 = 2 * (threadIdx.x >> 5);
+  const int64_t sh = blockIdx.x, states = p.seqs * p.H * p.P * p.N;
+  const int row0 = kJoinRows * blockIdx.y + r0;
+  float *at = p.ends + (sh * p.P + row0) * N + c;
+  auto in = [&](int r) { return row0 + r < p.P && c < N; };
+  auto fetch = [&](int s) {
+    const float *m = p.moves + ((s - 1) * p.seqs * p.H + sh) * N * N;
+    const uint32_t d = smem_addr(ms + ((s - 1) & 1) * N * N);
+    for (int k = threadIdx.x; k < N * N / 4; k += 256)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + 16 * k), "l"(m + 4 * k)
+                   : "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float4 v[2], next[2];
+  auto load = [&](float4 (&e)[2], int s) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      e[r] = in(r) ? *reinterpret_cast<const float4 *>(at + s * states + r * N)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  fetch(1);
+  load(v, 0);
+  load(next, 1);
+  for (int s = 1;; ++s) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      rows[c][r0 + r] = v[r].x;
+      rows[c + 1][r0 + r] = v[r].y;
+      rows[c + 2][r0 + r] = v[r].z;
+      rows[c + 3][r0 + r] = v[r].w;
+      v[r] = next[r];
+    }
+    if (s == p.segs - 1) break;
+    if (s < p.segs - 2) {
+      fetch(s + 1);
+      load(next, s + 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncthreads();
+    const float *m = ms + ((s - 1) & 1) * N * N + (c < N ? c : 0);
+#pragma unroll 8
+    for (int n = 0; n < N; ++n) {
+      const float2 h = *reinterpret_cast<const float2 *>(&rows[n][r0]);
+      const float4 x = *reinterpret_cast<const float4 *>(m + n * N);
+      v[0] = make_float4(fmaf(h.x, x.x, v[0].x), fmaf(h.x, x.y, v[0].y), fmaf(h.x, x.z, v[0].z),
+                         fmaf(h.x, x.w, v[0].w));
+      v[1] = make_float4(fmaf(h.y, x.x, v[1].x), fmaf(h.y, x.y, v[1].y), fmaf(h.y, x.z, v[1].z),
+                         fmaf(h.y, x.w, v[1].w));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      if (in(r)) *reinterpret_cast<float4 *>(at + s * states + r * N) = v[r];
+  }
+}
+
 // ------------------------------------------------------------ host side
 
 bool al16(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
@@ -1026,6 +1135,35 @@ bool delta_chunk_applies(const DeltaParams &p, bool in_bf16) {
          map_strides(p.sk, p.batch, p.L, p.G) && map_strides(p.sv, p.batch, p.L, p.H);
 }
 
+// A long sequence of few heads leaves SMs idle while its chain runs.  Cut into
+// segments, the first pass runs the first of them, and every other one but the
+// last from a zero state and from the unit rows: H_end = H_start M + B, B the
+// end from zero and M the transition.  The join gives every segment's start,
+// from which the second pass runs all but the first.  That is three times the
+// work on two chains of 1 / segs the length.
+// Times in chunks, a block's start taken as 3 of them and the join as 2.5 and
+// one more for every further segment.  8192 steps of 32 heads of 128 x 128 take
+// 361 us, 470 whole; of 8 heads 156, 450 whole; 2048 of 32 heads 109 and 123.
+int delta_segments(const DeltaParams &p, int sms, int *seg_chunks, int64_t *floats) {
+  const int64_t heads = p.seqs * p.H, tasks = heads * ((p.P + 127) / 128), nc = (p.L + C - 1) / C;
+  const auto waves = [&](int64_t blocks) { return (blocks + sms - 1) / sms; };
+  double best = 0.9 * waves(tasks) * (nc + 3);
+  int segs = 0;
+  for (int s = 3; s <= 32 && s <= nc && tasks < sms; ++s) {
+    const int64_t len = (nc + s - 1) / s;
+    if ((s - 1) * len >= nc) continue;  // an empty segment
+    const double t = (waves((s - 1) * tasks + (s - 2) * heads) + waves((s - 1) * tasks)) *
+                         (len + 3.0) + 2.5 + (s - 3);
+    if (t < best) {
+      best = t;
+      segs = s;
+      *seg_chunks = static_cast<int>(len);
+    }
+  }
+  *floats = segs ? heads * p.N * ((segs - 1) * p.P + (segs - 2) * p.N) : 0;
+  return segs;
+}
+
 cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t stream) {
   Maps maps;
   if (!encode(&maps.q, p.q, p.N, p.G, p.L, p.batch, p.sq, C) ||
@@ -1035,14 +1173,30 @@ cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t
   // y through tensor maps: bf16, rows on 16-byte boundaries
   const int y_tma = out_bf16 && al16(p.y) && map_strides(p.sy, p.batch, p.L, p.H) &&
                     encode(&maps.y, p.y, p.P, p.H, p.L, p.batch, p.sy, C);
-  const unsigned grid = static_cast<unsigned>(p.seqs * p.H * ((p.P + 127) / 128));
+  const int64_t heads = p.seqs * p.H, tasks = heads * ((p.P + 127) / 128);
   auto run = [&](auto kernel) {
     // per launch: the attribute belongs to the current device
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, kSmemBytes, stream>>>(maps, p, y_tma);
-    return cudaGetLastError();
+    auto pass = [&](int n, int64_t grid) {
+      DeltaParams q = p;
+      q.pass = n;
+      kernel<<<static_cast<unsigned>(grid), kThreads, kSmemBytes, stream>>>(maps, q, y_tma);
+      return cudaGetLastError();
+    };
+    if (!p.segs) return pass(0, tasks);
+    cudaError_t f = pass(1, (p.segs - 1) * tasks + (p.segs - 2) * heads);
+    if (f != cudaSuccess) return f;
+    const int join_smem = static_cast<int>(p.N * p.N) * 4 * (p.segs > 3 ? 2 : 1);
+    f = cudaFuncSetAttribute(delta_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             join_smem);
+    if (f != cudaSuccess) return f;
+    const dim3 join(static_cast<unsigned>(heads),
+                    static_cast<unsigned>((p.P + kJoinRows - 1) / kJoinRows));
+    delta_join_kernel<<<join, 256, join_smem, stream>>>(p);
+    if ((f = cudaGetLastError()) != cudaSuccess) return f;
+    return pass(2, (p.segs - 1) * tasks);
   };
   if (p.N <= 64)
     return out_bf16 ? run(delta_chunk_kernel<__nv_bfloat16, 4>) : run(delta_chunk_kernel<float, 4>);

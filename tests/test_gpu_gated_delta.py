@@ -12,6 +12,7 @@ their number.  A bf16 output is off by another half step:
 bf16 has 8 bits, so half a step is at most
 2^-8 of the value.
 """
+import ctypes
 import math
 
 import pytest
@@ -366,3 +367,103 @@ def test_layer():
         o = sss.gated_rmsnorm_fwd(y.flatten(-2), z, w2, group_size=P)
         want = gated_rmsnorm(y.flatten(-2).double(), z.double(), w2.double(), 1e-5, P, False)
         assert worst(o, want) <= 2.0 ** -8 + 64 * 2.0 ** -24
+
+
+def call(a):
+    """The call of filled arguments, without the binding's own workspace."""
+    stream = torch.cuda.current_stream().cuda_stream
+    return sss.load_library().gated_delta_fwd(ctypes.byref(a), stream)
+
+
+def workspace_bytes(a):
+    n = ctypes.c_size_t(0)
+    assert sss.load_library().mss_gated_delta_workspace_size(ctypes.byref(a), ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("size,h0", [
+    ((1, 1500, 1, 128, 1, 128), True), ((2, 1001, 3, 136, 1, 96), False),
+    ((1, 2048, 2, 64, 1, 64), True), ((1, 1217, 4, 72, 2, 40), True),
+    ((1, 1100, 1, 264, 1, 8), False), ((2, 2001, 3, 136, 1, 96), True),
+    ((1, 1700, 1, 264, 1, 8), True)])
+def test_segments(size, h0, out_dtype):
+    """Long sequences of few heads are cut into segments that run beside each
+    other: the float64 recurrence's values, every time the same bits.  (The
+    transition of a segment is a chunked state of its own, so a start off by
+    twice a chunked state's error joins the segment's.)"""
+    B, L, H, P, G, N = size
+    d = delta_inputs(*size, BF, seed=L, h0=h0)
+    y = torch.empty(B, L, H, P, device="cuda", dtype=out_dtype)
+    last = torch.empty(B, H, P, N, device="cuda")
+    got, gl = sss.gated_delta_fwd(**d, return_last_state=True, y=y, check_status=True)
+    yr, lr = gated_delta(**d)
+    extra = 3 * tolerance(N, L, F32, True)
+    assert worst(got, yr) <= extra + (2.0 ** -8 if out_dtype == BF else 0)
+    assert worst(gl, lr) <= extra
+    for _ in range(3):
+        again, al = sss.gated_delta_fwd(**d, return_last_state=True, out_dtype=out_dtype)
+        assert torch.equal(again, got) and torch.equal(al, gl)
+    # whole sequences, without a workspace
+    whole = sss.make_gated_delta_args(**d, y=torch.empty_like(y), last_state=last)
+    assert call(whole) == sss.MSS_OK
+    torch.cuda.synchronize()
+    assert worst(gl, last.double()) <= extra
+
+
+def test_segments_follow_the_sizes():
+    """Long sequences of few heads ask for a workspace; short ones, those that
+    fill the machine, packed ones and the recurrent plan do not."""
+    def size(B, L, H, dtype=BF, **kw):
+        d = delta_inputs(B, L, H, 64, 1, 64, dtype)
+        return workspace_bytes(sss.make_gated_delta_args(**d, **kw))
+    assert size(1, 1500, 1) > 0 and size(2, 2001, 3) > 0 and size(1, 1217, 4) > 0
+    cu = torch.tensor([0, 2000], dtype=torch.int32, device="cuda")
+    assert size(1, 500, 1) == size(1, 2000, 160) == size(1, 2000, 2, cu_seqlens=cu) == 0
+    assert size(1, 2000, 2, plan=1) == size(1, 2000, 2, F32) == 0
+
+
+def test_segments_in_place_and_workspace_errors():
+    d = delta_inputs(1, 1500, 2, 64, 1, 64, BF, h0=True)
+    want, wl = sss.gated_delta_fwd(**d, return_last_state=True)
+    state = d["h0"].clone()
+    got, _ = sss.gated_delta_fwd(**dict(d, h0=state), last_state=state, return_last_state=True)
+    assert torch.equal(got, want) and torch.equal(state, wl)
+    y = torch.full_like(want, 7.0)
+    a = sss.make_gated_delta_args(**d, y=y)
+    n = workspace_bytes(a)
+    ws = torch.full((n + 64,), 171, dtype=torch.uint8, device="cuda")
+    a.workspace, a.workspace_bytes = ws.data_ptr(), n - 1
+    assert call(a) == sss.MSS_ERR_WORKSPACE
+    a.workspace, a.workspace_bytes = ws.data_ptr() + 8, n
+    assert call(a) == sss.MSS_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+    assert (y == 7).all()
+    a.workspace = ws.data_ptr()
+    assert call(a) == sss.MSS_OK
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and (ws[n:] == 171).all()
+
+
+def test_segments_on_another_stream_and_in_graphs():
+    d = [delta_inputs(1, 1300, 2, 64, 1, 64, BF, seed=s, h0=True) for s in (1, 2)]
+    want = [sss.gated_delta_fwd(**x, return_last_state=True) for x in d]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in d]
+    for _ in range(5):
+        got = [sss.gated_delta_fwd(**x, return_last_state=True, stream=s)
+               for x, s in zip(d, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+    graphs, outs = [], []
+    for x in d:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(sss.gated_delta_fwd(**x, return_last_state=True))
+        graphs.append(graph)
+    for graph in graphs * 2:
+        graph.replay()
+    torch.cuda.synchronize()
+    for g, w in zip(outs, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
