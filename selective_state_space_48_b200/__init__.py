@@ -978,10 +978,13 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
     sequences into one row (batch 1); rows of y outside them are not
     written.  h0 and last_state: (sequences, nheads, headdim, dstate)
     float32, and may be one tensor.  Returns y (batch, L, nheads, headdim) in
-    ``out_dtype`` (and the final states when ``return_last_state``).
+    ``out_dtype`` (and the final states when ``return_last_state``).  Forward
+    only: no gradients pass.
     """
-    if not isinstance(v, torch.Tensor) or v.dim() != 4:
-        raise ValueError("v must have the dimensions (batch, seqlen, heads, width)")
+    if not isinstance(v, _Tensor) or not isinstance(q, _Tensor):
+        raise TypeError("q and v must be CUDA tensors")
+    if v.dim() != 4 or q.dim() != 4:
+        raise ValueError("q, k and v must have the dimensions (batch, seqlen, heads, width)")
     if y is None:
         y = _new(v, out_dtype)
     if return_last_state and last_state is None:

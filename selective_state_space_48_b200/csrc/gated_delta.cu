@@ -496,8 +496,10 @@ extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
       if (w != MSS_OK) return w;
       if (!al(a->workspace, 16)) return MSS_ERR_INVALID_ARG;
       if (a->workspace_bytes < static_cast<size_t>(floats) * 4) return MSS_ERR_WORKSPACE;
-      p.ends = static_cast<float *>(a->workspace);
-      p.moves = p.ends + (p.segs - 1) * p.seqs * p.H * p.P * p.N;
+      if (p.segs) {
+        p.ends = static_cast<float *>(a->workspace);
+        p.moves = p.ends + (p.segs - 1) * p.seqs * p.H * p.P * p.N;
+      }
     }
     return launch_delta_chunk(p, a->out_dtype == MSS_BF16, static_cast<cudaStream_t>(stream)) ==
                    cudaSuccess

@@ -190,3 +190,29 @@ def test_binding_refuses_host_tensors_and_shapes():
         sss._rows_of("x", torch.zeros(4, 6, 16)[:, :3])
     assert sss._rows_of("x", torch.zeros(4, 6, 32)[..., :16]) == (24, 32)
     assert sss._rows_of("x", torch.zeros(1, 6, 1, 16)[:, ::2]) == (3, 32)
+
+
+@pytest.mark.parametrize("n", ["q", "k", "v", "dt", "A", "beta"])
+def test_delta_binding_refuses_what_is_no_tensor(n):
+    """A missing tensor is a TypeError or ValueError that names the
+    arguments, with a final state asked for or not."""
+    d = dict(q=torch.zeros(1, 40, 1, 8), k=torch.zeros(1, 40, 1, 8), v=torch.zeros(1, 40, 1, 8),
+             dt=torch.zeros(1, 40, 1), A=torch.zeros(1), beta=torch.zeros(1, 40, 1))
+    for value in (None, 3.0):
+        for last in (False, True):
+            with pytest.raises((TypeError, ValueError)):
+                sss.gated_delta_fwd(**dict(d, **{n: value}), return_last_state=last)
+
+
+def test_delta_workspace_size_without_a_cut(lib):
+    """0 for packed sequences, fp32 and the recurrent plan, whatever the
+    device; refusals for sizes that a call refuses."""
+    n = ctypes.c_size_t(9)
+    size = lambda a: lib.mss_gated_delta_workspace_size(ctypes.byref(a), ctypes.byref(n))  # noqa: E731
+    for kw in (dict(batch=1, cu_seqlens=FAKE, num_seqs=3), dict(in_dtype=sss.MSS_F32),
+               dict(plan=sss.MSS_DELTA_RECURRENT), dict(dstate=200)):
+        n.value = 9
+        assert size(delta_args(**kw)) == sss.MSS_OK and n.value == 0
+    assert size(delta_args(dstate=300)) == UNS
+    assert size(delta_args(seqlen=0)) == INV
+    assert lib.mss_gated_delta_workspace_size(None, ctypes.byref(n)) == INV
