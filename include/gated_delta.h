@@ -54,7 +54,8 @@
  * Limits: dstate <= 256, any headdim.  Pointers are aligned to their element
  * size.  The chunked evaluation takes bf16 inputs with dstate a multiple of 8
  * up to 128, headdim a multiple of 8, q, k, v 16-byte aligned and their
- * strides multiples of 8; everything else runs the recurrent one.
+ * strides multiples of 8; everything else runs the recurrent one, or,
+ * with a workspace and dstate <= 128, is copied first.
  *
  * Ownership, streams and errors as in selective_scan.h: device pointers owned
  * by the caller, nothing allocated, work enqueued on `stream` without
@@ -118,10 +119,13 @@ typedef struct mss_delta_args {
 /* Forward over whole sequences: y (and last_state). */
 mss_status gated_delta_fwd(const mss_delta_args *args, void *stream);
 
-/* Bytes of workspace with which the chunked evaluation cuts long sequences of
- * few heads into segments that run beside each other (0: these sizes gain
- * nothing on the current device).  Without a workspace every sequence runs
- * whole; one that is too small is MSS_ERR_WORKSPACE. */
+/* Bytes of workspace that the call gains from on the current device (0:
+ * nothing).  With one, long sequences of few heads are cut into segments that
+ * run beside each other, and bf16 q, k, v of sizes, strides or addresses that
+ * the chunked evaluation does not take are copied for it (MSS_DELTA_AUTO).
+ * Without one every sequence runs whole, those recurrently.  One that is too
+ * small is MSS_ERR_WORKSPACE.  Of the tensors only the strides and whether
+ * pointers are 16-byte aligned matter here. */
 mss_status mss_gated_delta_workspace_size(const mss_delta_args *args, size_t *bytes);
 
 typedef struct mss_delta_update_args {

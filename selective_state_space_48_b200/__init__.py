@@ -936,16 +936,27 @@ def _workspace(nbytes, device, stream):
     return ws, ws.data_ptr()
 
 
-@functools.lru_cache(maxsize=1024)
-def _delta_workspace_bytes(batch, seqlen, nheads, headdim, dstate, device_index):
-    """Workspace bytes of a chunked call of these sizes on this device (0
-    also for sizes that the call itself refuses)."""
-    a, n = DeltaArgs(), ctypes.c_size_t(0)
-    a.batch, a.seqlen, a.nheads, a.headdim, a.ngroups = batch, seqlen, nheads, headdim, 1
-    a.dstate, a.in_dtype = dstate, MSS_BF16
+def _delta_room(a, device_index):
+    """Workspace bytes of a call on this device (0 also for one that the call
+    itself refuses)."""
+    n = ctypes.c_size_t(0)
     with torch.cuda.device(device_index):
         load_library().mss_gated_delta_workspace_size(ctypes.byref(a), ctypes.byref(n))
     return int(n.value)
+
+
+@functools.lru_cache(maxsize=1024)
+def _delta_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, seqs, plan,
+                           device_index):
+    """Workspace bytes of a call of dense bf16 tensors of these sizes."""
+    a = DeltaArgs()
+    a.batch, a.seqlen, a.nheads, a.headdim, a.ngroups = batch, seqlen, nheads, headdim, ngroups
+    a.dstate, a.in_dtype, a.plan = dstate, MSS_BF16, plan
+    a.cu_seqlens, a.num_seqs = (1 << 20, seqs) if seqs else (None, 0)
+    for n, heads, width in (("q", ngroups, dstate), ("k", ngroups, dstate),
+                            ("v", nheads, headdim)):
+        getattr(a, "stride_" + n)[:] = (seqlen * heads * width, heads * width, width)
+    return _delta_room(a, device_index)
 
 
 _pack_delta = _packer(DeltaArgs)
@@ -991,16 +1002,23 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
         seqs = v.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
         last_state = torch.empty((seqs, v.shape[2], v.shape[3], q.shape[-1]),
                                  dtype=torch.float32, device=v.device)
-    ws, room = None, (0, 0)
-    if cu_seqlens is None and v.dtype is torch.bfloat16 and v.is_cuda and \
-            plan != MSS_DELTA_RECURRENT:
-        nbytes = _delta_workspace_bytes(*v.shape, q.shape[-1], v.device.index)
+    values = _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y,
+                           last_state, cu_seqlens, plan, 0, (0, 0))
+    ws = None
+    if v.dtype is torch.bfloat16 and plan != MSS_DELTA_RECURRENT:
+        at = q.data_ptr() | k.data_ptr() | v.data_ptr()
+        for t in (h0, last_state):
+            at |= 0 if t is None else t.data_ptr()
+        if at & 15 == 0 and q.is_contiguous() and k.is_contiguous() and v.is_contiguous():
+            nbytes = _delta_workspace_bytes(
+                *v.shape, q.shape[2], q.shape[3],
+                0 if cu_seqlens is None else cu_seqlens.shape[0] - 1, plan, v.device.index)
+        else:
+            nbytes = _delta_room(DeltaArgs.from_buffer_copy(_pack_delta(*values)), v.device.index)
         if nbytes:
             ws, pws = _workspace(nbytes, v.device, stream)
-            room = (pws, nbytes)
-    _enqueue("gated_delta_fwd", _pack_delta(*_delta_values(
-        q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y, last_state,
-        cu_seqlens, plan, 0, room)), q.device, stream)
+            values = (*values[:-2], pws, nbytes)
+    _enqueue("gated_delta_fwd", _pack_delta(*values), q.device, stream)
     if check_status:
         with _on_device(q.device, stream) as s:
             rc = load_library().mss_gated_delta_status(_stream_handle(s))

@@ -41,6 +41,11 @@ constexpr int kThreads = 128;
 // of one sequence 8.0 / 16.7 at 16 steps, 13.5 / 16.3 at 32, 24 / 16 at 64; of
 // 8 sequences 24 / 33, 42 / 32, 79 / 33; of 32 86 / 119, 156 / 118, 300 / 127.
 constexpr int64_t kChunkSteps = 32;
+// ... and where q, k, v are copied for it first (sizes, strides or addresses
+// that tensor maps do not take): one sequence of 32 heads of 100 x 100, steps
+// against copy and chunks, us: 20 / 16 at 48 steps, 27 / 17 at 64, 48 / 22 at
+// 128; 8 of 2048 2607 / 519.
+constexpr int64_t kCopySteps = 48;
 
 // Four columns from `col` of a row of n columns: one vector load where VEC,
 // else element by element with zeros past the end.
@@ -400,13 +405,30 @@ mss_status check_sizes(int64_t batch, int64_t L, int64_t H, int64_t P, int64_t G
   return MSS_OK;
 }
 
-// The cut of the call's sequences on the current device: p.segs, p.seg_chunks.
-mss_status segments(DeltaParams &p, int64_t *floats) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return MSS_ERR_CUDA;
-  p.segs = delta_segments(p, sms, &p.seg_chunks, floats);
+bool chunked(const DeltaParams &p, int plan, int64_t steps) {
+  return plan == MSS_DELTA_CHUNKED ||
+         (plan == MSS_DELTA_AUTO && p.L / (p.cu ? p.seqs : 1) >= steps);
+}
+
+// What a call does with a workspace: copies of q, k, v that tensor maps can
+// read, and the segments of its sequences (p.segs, p.seg_chunks; on the current
+// device).
+struct Room {
+  int64_t copies = 0, segments = 0;  // bytes
+  int64_t bytes() const { return copies + segments; }
+};
+mss_status workspace(DeltaParams &p, int plan, bool bf16, bool applies, Room *room) {
+  const bool copies = !applies && bf16 && p.N <= 128 && chunked(p, plan, kCopySteps);
+  if (copies) room->copies = (delta_copy_bytes(p) + 15) / 16 * 16;
+  if (!p.cu && (copies || (applies && chunked(p, plan, kChunkSteps)))) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return MSS_ERR_CUDA;
+    int64_t floats = 0;
+    p.segs = delta_segments(p, sms, &p.seg_chunks, &floats);
+    room->segments = 4 * floats;
+  }
   return MSS_OK;
 }
 
@@ -429,18 +451,47 @@ cudaError_t launch_delta_recurrent(const DeltaParams &p, bool in_bf16, bool out_
 
 using namespace sss48;
 
-extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
-  sss48::NvtxRange range("gated_delta_fwd");
+namespace {
+
+// sizes, strides and pointers of a call's tensors
+mss_status sizes(const mss_delta_args *a, DeltaParams *p) {
   if (!a) return MSS_ERR_INVALID_ARG;
   const bool packed = a->cu_seqlens != nullptr;
   if (packed ? (a->num_seqs < 1 || a->batch != 1 || !al(a->cu_seqlens, 4)) : a->num_seqs != 0)
     return MSS_ERR_INVALID_ARG;
-  const int64_t seqs = packed ? a->num_seqs : a->batch;
-  const mss_status st = check_sizes(seqs, a->seqlen, a->nheads, a->headdim, a->ngroups, a->dstate,
-                                    a->in_dtype, a->out_dtype);
+  if (a->plan < MSS_DELTA_AUTO || a->plan > MSS_DELTA_CHUNKED) return MSS_ERR_INVALID_ARG;
+  p->seqs = packed ? a->num_seqs : a->batch;
+  const mss_status st = check_sizes(p->seqs, a->seqlen, a->nheads, a->headdim, a->ngroups,
+                                    a->dstate, a->in_dtype, a->out_dtype);
+  if (st != MSS_OK) return st;
+  p->batch = a->batch;
+  p->L = a->seqlen;
+  p->H = a->nheads;
+  p->P = a->headdim;
+  p->G = a->ngroups;
+  p->N = a->dstate;
+  p->q = a->q;
+  p->k = a->k;
+  p->v = a->v;
+  p->h0 = a->h0;
+  p->last = a->last_state;
+  p->cu = a->cu_seqlens;
+  for (int i = 0; i < 3; ++i) {
+    p->sq[i] = a->stride_q[i];
+    p->sk[i] = a->stride_k[i];
+    p->sv[i] = a->stride_v[i];
+  }
+  return MSS_OK;
+}
+
+}  // namespace
+
+extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
+  sss48::NvtxRange range("gated_delta_fwd");
+  DeltaParams p{};
+  const mss_status st = sizes(a, &p);
   if (st != MSS_OK) return st;
   if (!a->q || !a->k || !a->v || !a->dt || !a->A || !a->beta || !a->y) return MSS_ERR_INVALID_ARG;
-  if (a->plan < MSS_DELTA_AUTO || a->plan > MSS_DELTA_CHUNKED) return MSS_ERR_INVALID_ARG;
   const size_t ie = a->in_dtype == MSS_BF16 ? 2 : 4, oe = a->out_dtype == MSS_BF16 ? 2 : 4;
   if (!al(a->q, ie) || !al(a->k, ie) || !al(a->v, ie) || !al(a->dt, ie) || !al(a->beta, ie) ||
       !al(a->y, oe) || !al(a->A, 4) || !al(a->dt_bias, 4) || !al(a->h0, 4) ||
@@ -452,17 +503,6 @@ extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
       !strides_ok(a->stride_v, nh, a->headdim, false) || !strides_ok(a->stride_dt, nh, 1, false) ||
       !strides_ok(a->stride_beta, nh, 1, false) || !strides_ok(a->stride_y, nh, a->headdim, true))
     return MSS_ERR_INVALID_ARG;
-  DeltaParams p{};
-  p.seqs = seqs;
-  p.batch = a->batch;
-  p.L = a->seqlen;
-  p.H = a->nheads;
-  p.P = a->headdim;
-  p.G = a->ngroups;
-  p.N = a->dstate;
-  p.q = a->q;
-  p.k = a->k;
-  p.v = a->v;
   p.dt = a->dt;
   p.beta = a->beta;
   p.A = a->A;
@@ -470,41 +510,35 @@ extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
   p.softplus = a->dt_softplus ? 1 : 0;
   p.sigmoid = a->beta_sigmoid ? 1 : 0;
   p.scale = a->scale;
-  p.h0 = a->h0;
   p.y = a->y;
-  p.last = a->last_state;
   for (int i = 0; i < 3; ++i) {
-    p.sq[i] = a->stride_q[i];
-    p.sk[i] = a->stride_k[i];
-    p.sv[i] = a->stride_v[i];
     p.sdt[i] = a->stride_dt[i];
     p.sbeta[i] = a->stride_beta[i];
     p.sy[i] = a->stride_y[i];
   }
-  p.cu = a->cu_seqlens;
   p.spin_ns = a->spin_timeout_ns ? a->spin_timeout_ns : 2000000000ull;
   const bool bf16 = a->in_dtype == MSS_BF16;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
   const bool applies = delta_chunk_applies(p, bf16);
   if (a->plan == MSS_DELTA_CHUNKED && !applies) return MSS_ERR_UNSUPPORTED;
-  if (applies && (a->plan == MSS_DELTA_CHUNKED ||
-                  (a->plan == MSS_DELTA_AUTO && p.L / (packed ? seqs : 1) >= kChunkSteps))) {
+  Room room;
+  if (a->workspace) {
+    const mss_status w = workspace(p, a->plan, bf16, applies, &room);
+    if (w != MSS_OK) return w;
+    if (!al(a->workspace, 16)) return MSS_ERR_INVALID_ARG;
+    if (a->workspace_bytes < static_cast<size_t>(room.bytes())) return MSS_ERR_WORKSPACE;
+  }
+  if (room.copies || (applies && chunked(p, a->plan, kChunkSteps))) {
     p.status = delta_status_word();
     if (!p.status) return MSS_ERR_CUDA;
-    if (a->workspace && !packed) {
-      int64_t floats = 0;
-      const mss_status w = segments(p, &floats);
-      if (w != MSS_OK) return w;
-      if (!al(a->workspace, 16)) return MSS_ERR_INVALID_ARG;
-      if (a->workspace_bytes < static_cast<size_t>(floats) * 4) return MSS_ERR_WORKSPACE;
-      if (p.segs) {
-        p.ends = static_cast<float *>(a->workspace);
-        p.moves = p.ends + (p.segs - 1) * p.seqs * p.H * p.P * p.N;
-      }
+    char *ws = static_cast<char *>(a->workspace);
+    if (room.copies && launch_delta_copy(&p, ws, on) != cudaSuccess) return MSS_ERR_CUDA;
+    if (p.segs) {
+      p.ends = reinterpret_cast<float *>(ws + room.copies);
+      p.moves = p.ends + (p.segs - 1) * p.seqs * p.H * p.P * p.N;
     }
-    return launch_delta_chunk(p, a->out_dtype == MSS_BF16, static_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
-               ? MSS_OK
-               : MSS_ERR_CUDA;
+    return launch_delta_chunk(p, a->out_dtype == MSS_BF16, on) == cudaSuccess ? MSS_OK
+                                                                            : MSS_ERR_CUDA;
   }
   return launch_delta_recurrent(p, a->in_dtype == MSS_BF16, a->out_dtype == MSS_BF16,
                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -513,23 +547,14 @@ extern "C" mss_status gated_delta_fwd(const mss_delta_args *a, void *stream) {
 }
 
 extern "C" mss_status mss_gated_delta_workspace_size(const mss_delta_args *a, size_t *bytes) {
-  if (!a || !bytes) return MSS_ERR_INVALID_ARG;
-  mss_status st = check_sizes(a->cu_seqlens ? a->num_seqs : a->batch, a->seqlen, a->nheads,
-                              a->headdim, a->ngroups, a->dstate, a->in_dtype, a->out_dtype);
-  if (st != MSS_OK) return st;
-  *bytes = 0;
-  if (a->cu_seqlens || a->in_dtype != MSS_BF16 || a->dstate > 128 ||
-      a->plan == MSS_DELTA_RECURRENT)
-    return MSS_OK;
+  if (!bytes) return MSS_ERR_INVALID_ARG;
   DeltaParams p{};
-  p.seqs = p.batch = a->batch;
-  p.L = a->seqlen;
-  p.H = a->nheads;
-  p.P = a->headdim;
-  p.N = a->dstate;
-  int64_t floats = 0;
-  if ((st = segments(p, &floats)) != MSS_OK) return st;
-  *bytes = static_cast<size_t>(floats) * 4;
+  mss_status st = sizes(a, &p);
+  if (st != MSS_OK) return st;
+  const bool bf16 = a->in_dtype == MSS_BF16;
+  Room room;
+  if ((st = workspace(p, a->plan, bf16, delta_chunk_applies(p, bf16), &room)) != MSS_OK) return st;
+  *bytes = static_cast<size_t>(room.bytes());
   return MSS_OK;
 }
 

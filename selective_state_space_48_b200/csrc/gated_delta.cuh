@@ -61,6 +61,10 @@ cudaError_t launch_delta_recurrent(const DeltaParams &p, bool in_bf16, bool out_
 // true where the chunked kernel applies to these types, sizes and addresses
 bool delta_chunk_applies(const DeltaParams &p, bool in_bf16);
 cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t stream);
+// bytes of copies of q, k, v that tensor maps can read, and the launch that
+// makes them at `to` and points p at them
+int64_t delta_copy_bytes(const DeltaParams &p);
+cudaError_t launch_delta_copy(DeltaParams *p, void *to, cudaStream_t stream);
 // segments that sequences of these sizes are best cut into on `sms` SMs (0:
 // none), their length in chunks, and the floats of workspace that takes
 int delta_segments(const DeltaParams &p, int sms, int *seg_chunks, int64_t *floats);

@@ -48,6 +48,8 @@
 // wait is bounded as in tcgen05.cuh, so no block can hang.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "device_math.cuh"
 #include "gated_delta.cuh"
 #include "tcgen05.cuh"
@@ -367,7 +369,8 @@ __device__ __forceinline__ constexpr uint32_t kslice(int k) {
 // y_tma: whole chunks of y go out through their Q tile and a TMA store (bf16
 // rows that a tensor map takes): 16 two-byte stores of a thread straight to
 // memory took 1.3 us of a chunk's 4.5.
-template <typename OutT, int NK>
+// VEC: states in rows of 16-byte vectors.
+template <typename OutT, int NK, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p, const int y_tma) {
   constexpr uint32_t idH = idesc_bf16(128, 16 * NK, 0, 1);  // the second as stored by step
@@ -716,8 +719,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (h0 && row < P && 32 * e + j < N)
-        v = __ldcs(reinterpret_cast<const float4 *>(h0 + base + j));
+      if (h0 && row < P && 32 * e + j < N) {
+        if constexpr (VEC) {
+          v = __ldcs(reinterpret_cast<const float4 *>(h0 + base + j));
+        } else {
+          float *f = reinterpret_cast<float *>(&v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (32 * e + j + k < N) f[k] = h0[base + j + k];
+        }
+      }
       H[j] = v.x;
       H[j + 1] = v.y;
       H[j + 2] = v.z;
@@ -866,10 +877,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (last && row < P) {
 #pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        if (32 * e + j < N)
+      for (int j = 0; j < 32; ++j) {
+        if (32 * e + j >= N) continue;
+        if constexpr (!VEC)
+          last[base + j] = H[j];
+        else if (j % 4 == 0)
           __stcs(reinterpret_cast<float4 *>(last + base + j),
                  make_float4(H[j], H[j + 1], H[j + 2], H[j + 3]));
+      }
     }
   } else if (warp >= 20) {
     // ------------------------------------- what does not depend on H
@@ -1088,6 +1103,43 @@ __global__ void __launch_bounds__(256) delta_join_kernel(const DeltaParams p) {
   }
 }
 
+// Copies of q, k, v (blockIdx.y) whose rows start on 16 bytes, for sizes and
+// views that tensor maps do not take: a warp four rows, two channels of a lane.
+constexpr int kCopyWarps = 8, kCopyRows = 4;
+__global__ void __launch_bounds__(32 * kCopyWarps)
+    delta_copy_kernel(const __grid_constant__ DeltaParams p, __nv_bfloat16 *q, __nv_bfloat16 *k,
+                      __nv_bfloat16 *v) {
+  const int which = blockIdx.y, lane = threadIdx.x & 31;
+  const __nv_bfloat16 *src =
+      static_cast<const __nv_bfloat16 *>(which == 0 ? p.q : which == 1 ? p.k : p.v);
+  __nv_bfloat16 *dst = which == 0 ? q : which == 1 ? k : v;
+  const int64_t *st = which == 0 ? p.sq : which == 1 ? p.sk : p.sv;
+  const int64_t heads = which == 2 ? p.H : p.G, width = which == 2 ? p.P : p.N;
+  const int64_t pitch = (width + 7) / 8 * 8, rows = p.batch * p.L * heads;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyWarps * kCopyRows;
+  for (int64_t r0 = (static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5)) * kCopyRows;
+       r0 < rows; r0 += step) {
+    const __nv_bfloat16 *from[kCopyRows];
+#pragma unroll
+    for (int i = 0; i < kCopyRows; ++i) {
+      const int64_t r = r0 + i < rows ? r0 + i : rows - 1, t = r / heads, b = t / p.L;
+      from[i] = src + b * st[0] + (t - b * p.L) * st[1] + (r - t * heads) * st[2];
+    }
+    for (int64_t c = 2 * lane; c < width; c += 64) {
+      __nv_bfloat162 two[kCopyRows];
+#pragma unroll
+      for (int i = 0; i < kCopyRows; ++i) {
+        two[i].x = from[i][c];
+        two[i].y = c + 1 < width ? from[i][c + 1] : __float2bfloat16(0.f);
+      }
+#pragma unroll
+      for (int i = 0; i < kCopyRows; ++i)
+        if (r0 + i < rows)
+          *reinterpret_cast<__nv_bfloat162 *>(dst + (r0 + i) * pitch + c) = two[i];
+    }
+  }
+}
+
 // ------------------------------------------------------------ host side
 
 bool al16(const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
@@ -1135,6 +1187,35 @@ bool delta_chunk_applies(const DeltaParams &p, bool in_bf16) {
          map_strides(p.sk, p.batch, p.L, p.G) && map_strides(p.sv, p.batch, p.L, p.H);
 }
 
+namespace {
+int64_t copy_pitch(int64_t width) { return (width + 7) / 8 * 8; }
+}  // namespace
+
+int64_t delta_copy_bytes(const DeltaParams &p) {
+  return 2 * p.batch * p.L * (2 * p.G * copy_pitch(p.N) + p.H * copy_pitch(p.P));
+}
+
+cudaError_t launch_delta_copy(DeltaParams *p, void *to, cudaStream_t stream) {
+  const int64_t n = copy_pitch(p->N), w = copy_pitch(p->P), rows = p->batch * p->L;
+  __nv_bfloat16 *q = static_cast<__nv_bfloat16 *>(to), *k = q + rows * p->G * n,
+                *v = k + rows * p->G * n;
+  const int64_t per = kCopyWarps * kCopyRows, blocks = (rows * p->H + per - 1) / per;
+  delta_copy_kernel<<<dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 3),
+                      32 * kCopyWarps, 0, stream>>>(*p, q, k, v);
+  p->q = q;
+  p->k = k;
+  p->v = v;
+  const auto dense = [&](int64_t (&s)[3], int64_t heads, int64_t pitch) {
+    s[0] = p->L * heads * pitch;
+    s[1] = heads * pitch;
+    s[2] = pitch;
+  };
+  dense(p->sq, p->G, n);
+  dense(p->sk, p->G, n);
+  dense(p->sv, p->H, w);
+  return cudaGetLastError();
+}
+
 // A long sequence of few heads leaves SMs idle while its chain runs.  Cut into
 // segments, the first pass runs the first of them, and every other one but the
 // last from a zero state and from the unit rows: H_end = H_start M + B, B the
@@ -1149,7 +1230,8 @@ int delta_segments(const DeltaParams &p, int sms, int *seg_chunks, int64_t *floa
   const auto waves = [&](int64_t blocks) { return (blocks + sms - 1) / sms; };
   double best = 0.9 * waves(tasks) * (nc + 3);
   int segs = 0;
-  for (int s = 3; s <= 32 && s <= nc && tasks < sms; ++s) {
+  // (the join moves rows of vectors)
+  for (int s = 3; s <= 32 && s <= nc && tasks < sms && p.N % 4 == 0; ++s) {
     const int64_t len = (nc + s - 1) / s;
     if ((s - 1) * len >= nc) continue;  // an empty segment
     const double t = (waves((s - 1) * tasks + (s - 2) * heads) + waves((s - 1) * tasks)) *
@@ -1198,9 +1280,17 @@ cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t
     if ((f = cudaGetLastError()) != cudaSuccess) return f;
     return pass(2, (p.segs - 1) * tasks);
   };
-  if (p.N <= 64)
-    return out_bf16 ? run(delta_chunk_kernel<__nv_bfloat16, 4>) : run(delta_chunk_kernel<float, 4>);
-  return out_bf16 ? run(delta_chunk_kernel<__nv_bfloat16, 8>) : run(delta_chunk_kernel<float, 8>);
+  auto by_state = [&](auto out, auto nk) {
+    using O = decltype(out);
+    constexpr int NK = decltype(nk)::value;
+    return p.N % 4 == 0 && al16(p.h0) && al16(p.last) ? run(delta_chunk_kernel<O, NK, true>)
+                                                      : run(delta_chunk_kernel<O, NK, false>);
+  };
+  auto by_width = [&](auto nk) {
+    return out_bf16 ? by_state(__nv_bfloat16(), nk) : by_state(float(), nk);
+  };
+  return p.N <= 64 ? by_width(std::integral_constant<int, 4>())
+                   : by_width(std::integral_constant<int, 8>());
 }
 
 }  // namespace sss48

@@ -467,3 +467,89 @@ def test_segments_on_another_stream_and_in_graphs():
     torch.cuda.synchronize()
     for g, w in zip(outs, want):
         assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+# batch, L, heads, headdim, groups, dstate that no tensor map takes as they lie
+ODD_SIZES = [(2, 130, 3, 33, 1, 31), (1, 64, 2, 20, 2, 20), (3, 300, 4, 77, 2, 70),
+             (1, 1500, 1, 100, 1, 36), (1, 1700, 2, 129, 1, 127), (2, 200, 2, 1, 1, 1)]
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("size", ODD_SIZES)
+def test_copied_sizes(size, out_dtype):
+    """Odd sizes in bf16 are copied into rows that the chunked evaluation
+    takes, states of odd rows among them."""
+    d = delta_inputs(*size, BF, seed=size[1], h0=size[0] != 2)
+    N, L = size[5], size[1]
+    assert workspace_bytes(sss.make_gated_delta_args(**d, y=torch.empty_like(d["v"]))) > 0
+    y, last = sss.gated_delta_fwd(**d, return_last_state=True, out_dtype=out_dtype,
+                                  check_status=True)
+    yr, lr = gated_delta(**d)
+    tol = 3 * tolerance(N, L, F32, True)  # (as for segments)
+    assert worst(y, yr) <= tol + (2.0 ** -8 if out_dtype == BF else 0.0)
+    assert worst(last, lr) <= tol
+    again, al = sss.gated_delta_fwd(**d, return_last_state=True, out_dtype=out_dtype)
+    assert torch.equal(again, y) and torch.equal(al, last)
+
+
+def test_copied_packed_rows_and_views():
+    """Packed odd sizes with rows behind the last sequence; q, k, v as odd
+    slices of one projection, y a slice at an odd place."""
+    cu = torch.tensor([0, 70, 70, 71, 200, 328], dtype=torch.int32, device="cuda")
+    d = delta_inputs(1, 340, 2, 45, 1, 50, BF, h0=True, seqs=5)
+    for n in ("q", "k", "v", "dt", "beta"):
+        d[n][:, 328:] = float("nan")
+    y = torch.full((1, 340, 2, 45), 7.0, device="cuda", dtype=BF)
+    y, last = sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=True, y=y)
+    yr, lr = gated_delta(**d, cu_seqlens=cu)
+    assert worst(y[0, :328], yr[0, :328]) <= tolerance(50, 130, BF, True)
+    assert worst(last, lr) <= tolerance(50, 130, F32, True)
+    assert (y[0, 328:] == 7).all()
+    d = delta_inputs(2, 150, 4, 30, 2, 25, BF, h0=True)
+    want, wl = sss.gated_delta_fwd(**d, return_last_state=True, out_dtype=BF)
+    wide = torch.cat([d[n].flatten(2) for n in ("q", "k", "v")], -1)
+    q, k, v = wide.split([50, 50, 120], -1)
+    views = dict(d, q=q.unflatten(2, (2, 25)), k=k.unflatten(2, (2, 25)), v=v.unflatten(2, (4, 30)))
+    buf = torch.full((2, 150, 4, 33), 7.0, device="cuda", dtype=BF)
+    got, gl = sss.gated_delta_fwd(**views, return_last_state=True, y=buf[..., 1:31])
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    assert (buf[..., :1] == 7).all() and (buf[..., 31:] == 7).all()
+
+
+def test_copies_keep_inside_their_workspace():
+    d = delta_inputs(1, 100, 2, 33, 1, 31, BF)
+    want = sss.gated_delta_fwd(**d)
+    y = torch.full_like(want, 7.0)
+    a = sss.make_gated_delta_args(**d, y=y)
+    n = workspace_bytes(a)
+    ws = torch.full((n + 64,), 171, dtype=torch.uint8, device="cuda")
+    a.workspace, a.workspace_bytes = ws.data_ptr(), n - 1
+    assert call(a) == sss.MSS_ERR_WORKSPACE
+    a.workspace_bytes = n
+    assert call(a) == sss.MSS_OK
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and (ws[n:] == 171).all()
+
+
+def test_even_sizes_at_odd_places():
+    """Sizes that the chunked evaluation takes, in views and states whose
+    addresses or strides it does not: the same values."""
+    d = delta_inputs(1, 1500, 1, 64, 1, 64, BF, h0=True)
+    want, wl = sss.gated_delta_fwd(**d, return_last_state=True)
+    tol = 6 * tolerance(64, 1500, F32, True)  # (two evaluations)
+    shifted = dict(d)
+    for n in ("q", "k", "v"):
+        buf = torch.zeros(d[n].numel() + 3, device="cuda", dtype=BF)
+        buf[3:] = d[n].flatten()
+        shifted[n] = buf[3:].view_as(d[n])
+    state = torch.zeros(64 * 64 + 1, device="cuda")
+    state[1:] = d["h0"].flatten()
+    state = state[1:].view_as(d["h0"])
+    wide = torch.zeros(1, 1500, 1, 67, device="cuda", dtype=BF)
+    wide[..., 1:65] = d["v"]
+    for odd in (shifted, dict(d, h0=state), dict(d, v=wide[..., 1:65]),
+                dict(d, k=d["k"].expand(1, 1500, 1, 64), v=wide[..., 1:65], h0=state)):
+        y, last = sss.gated_delta_fwd(**odd, return_last_state=True)
+        assert worst(y, want.double()) <= tol and worst(last, wl.double()) <= tol
+    y, _ = sss.gated_delta_fwd(**dict(d, h0=state), last_state=state, return_last_state=True)
+    assert worst(y, want.double()) <= tol and worst(state, wl.double()) <= tol
