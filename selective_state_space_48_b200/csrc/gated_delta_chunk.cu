@@ -1252,8 +1252,9 @@ cudaError_t launch_delta_chunk(const DeltaParams &p, bool out_bf16, cudaStream_t
       !encode(&maps.k, p.k, p.N, p.G, p.L, p.batch, p.sk, C) ||
       !encode(&maps.v, p.v, p.P, p.H, p.L, p.batch, p.sv, C))
     return cudaErrorInvalidValue;
-  // y through tensor maps: bf16, rows on 16-byte boundaries
-  const int y_tma = out_bf16 && al16(p.y) && map_strides(p.sy, p.batch, p.L, p.H) &&
+  // y through tensor maps: bf16, rows that start and end on 16-byte boundaries
+  // (a store writes whole 16 bytes, past a width that does not)
+  const int y_tma = out_bf16 && p.P % 8 == 0 && al16(p.y) && map_strides(p.sy, p.batch, p.L, p.H) &&
                     encode(&maps.y, p.y, p.P, p.H, p.L, p.batch, p.sy, C);
   const int64_t heads = p.seqs * p.H, tasks = heads * ((p.P + 127) / 128);
   auto run = [&](auto kernel) {

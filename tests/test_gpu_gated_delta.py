@@ -514,6 +514,14 @@ def test_copied_packed_rows_and_views():
     got, gl = sss.gated_delta_fwd(**views, return_last_state=True, y=buf[..., 1:31])
     assert torch.equal(got, want) and torch.equal(gl, wl)
     assert (buf[..., :1] == 7).all() and (buf[..., 31:] == 7).all()
+    # rows of y on 16 bytes, their width not: nothing written beside it
+    for width in (30, 25):
+        buf = torch.full((2, 150, 4, 40), 7.0, device="cuda", dtype=BF)
+        got, _ = sss.gated_delta_fwd(**dict(d, v=d["v"][..., :width], h0=None),
+                                     return_last_state=True, y=buf[..., :width])
+        want, _ = sss.gated_delta_fwd(**dict(d, v=d["v"][..., :width], h0=None),
+                                      return_last_state=True, out_dtype=BF)
+        assert torch.equal(got, want) and (buf[..., width:] == 7).all()
 
 
 def test_copies_keep_inside_their_workspace():
