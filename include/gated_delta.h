@@ -34,7 +34,12 @@
  *              workspace, long sequences of few heads are cut into segments
  *              that run beside each other: the state passes a segment as
  *              S_end = S_start M + B, with M and B from a first pass.
- * A NaN or an infinity in a step's inputs spoils that head from the step on
+ *              The running sums c are pairs of fp32 values, so a decay is as
+ *              exact behind a step that wipes the state as anywhere else;
+ *              log2 a of a step counts as -300 where it is below (a is 0 in
+ *              fp32 from -150 on).
+ * A NaN in a step's inputs, or an infinity (but in a Delta_t A[h] of minus
+ * infinity, which is a decay of 0), spoils that head from the step on
  * (recurrent) or from the first step of its chunk on (chunked), nothing else.
  *
  * Layouts (the last dimension contiguous; batch, step and head strides in

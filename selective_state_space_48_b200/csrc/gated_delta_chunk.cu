@@ -27,6 +27,10 @@
 // at most): a product with an exact operand takes two products, one of two
 // such pairs three (lo lo is left out).  H itself stays in fp32 registers and
 // is added to there, not in the tensor cores' accumulators.
+// The sums c are pairs of fp32 values: a decay is the power of the difference
+// of two of them, and one word alone, rounded to 2^-24 of its size, takes that
+// from every decay behind a hard one (after a step of log2 a = -2300 outputs
+// were off by 2e-4 up to the chunk's end, after one of -2.3e6 by 8 %).
 //
 // Roles (28 warps, one block per SM: the sequence, head and 128 rows):
 //   warps 0, 3    TMA loads of the K, Q tiles (three stages); of V (one), and
@@ -76,8 +80,8 @@ constexpr int oScr = oT + 4 * kHalf;  // scratch of the inverse, for each group
 // transposed, then T in the diagonal ones; A21 T11
 constexpr int kLd = 40, kBlk = 32 * kLd;
 constexpr int bA11 = 0, bA22 = 1, bA21 = 2, bZ = 3, kScr = 4 * kBlk;
-constexpr int oGate = oScr + 2 * kScr * 4;  // two of (b, c) [C]
-constexpr int kGate = 2 * C * 4;
+constexpr int oGate = oScr + 2 * kScr * 4;  // two of (b, -c hi, -c lo) [C]
+constexpr int kGate = 3 * C * 4;
 constexpr int oDecay = oGate + 2 * kGate;  // three of (2^(c_last - c), 2^c, scale 2^c) [C]
 constexpr int kDecay = 3 * C * 4;
 constexpr int oBar = oDecay + 3 * kDecay;
@@ -181,6 +185,18 @@ struct Waits {
 struct Maps {
   CUtensorMap q, k, v, y;
 };
+
+// A step's log2 decay is taken as at least this: two to it times any fp32 value
+// is 0, and 64 of them leave the pairs of the sums exact to 2^-30.  (As a
+// comparison that lets NaN pass.)
+constexpr float kLeastLog2 = -300.f;
+
+// s = a + b; returned: what that rounded off
+__device__ __forceinline__ float two_sum(float a, float b, float &s) {
+  s = a + b;
+  const float t = s - a;
+  return (a - (s - t)) + (b - t);
+}
 
 __device__ unsigned g_delta_status;
 
@@ -671,38 +687,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nc > 0) raw(0);
     for (int i = 0; i < nc; ++i) {
       const int left = total - i * C;
-      float g2[2], bt[2];
+      float g2[2], lo[2], bt[2];  // g2 + lo: the running sums
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        g2[k] = bt[k] = 0.f;
+        g2[k] = lo[k] = bt[k] = 0.f;
         if (32 * k + lane < left)
           delta_gates<__nv_bfloat16>(p, __uint_as_float(static_cast<uint32_t>(rd[k]) << 16),
                                      __uint_as_float(static_cast<uint32_t>(rb[k]) << 16), A2, bias,
                                      g2[k], bt[k]);
+        if (g2[k] < kLeastLog2) g2[k] = kLeastLog2;
       }
       raw(i + 1);
+      auto add = [&](int k, float hi_before, float lo_before) {
+        const float r = two_sum(hi_before, g2[k], g2[k]);
+        lo[k] += lo_before + r;
+      };
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const float x0 = __shfl_up_sync(0xffffffffu, g2[0], o);
-        const float x1 = __shfl_up_sync(0xffffffffu, g2[1], o);
-        if (lane >= o) {
-          g2[0] += x0;
-          g2[1] += x1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float x = __shfl_up_sync(0xffffffffu, g2[k], o);
+          const float xl = __shfl_up_sync(0xffffffffu, lo[k], o);
+          if (lane >= o) add(k, x, xl);
         }
       }
-      g2[1] += __shfl_sync(0xffffffffu, g2[0], 31);
+      add(1, __shfl_sync(0xffffffffu, g2[0], 31), __shfl_sync(0xffffffffu, lo[0], 31));
       const float end1 = __shfl_sync(0xffffffffu, g2[1], 31);
+      const float end1l = __shfl_sync(0xffffffffu, lo[1], 31);
       if (i >= 2) sy.wait(kFreeG + (i & 1), (i / 2 - 1) & 1);
       if (i >= 3) sy.wait(kFreeD + i % 3, (i / 3 - 1) & 1);
-      float *beta_s = reinterpret_cast<float *>(sm + oGate + (i & 1) * kGate), *cum_s = beta_s + C;
+      float *beta_s = reinterpret_cast<float *>(sm + oGate + (i & 1) * kGate), *neg_s = beta_s + C;
       float *du = reinterpret_cast<float *>(sm + oDecay + (i % 3) * kDecay);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int t = 32 * k + lane;
-        const float eo = ex2_mufu(g2[k]);
-        cum_s[t] = g2[k];
+        const float eo = ex2_mufu(g2[k] + lo[k]);
+        neg_s[t] = -g2[k];
+        neg_s[C + t] = -lo[k];
         beta_s[t] = bt[k];
-        du[t] = ex2_mufu(end1 - g2[k]);
+        du[t] = ex2_mufu((end1 - g2[k]) + (end1l - lo[k]));
         du[C + t] = eo;
         du[2 * C + t] = p.scale * eo;
       }
@@ -894,7 +917,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *scr = reinterpret_cast<float *>(sm + oScr) + gr * kScr;
     unsigned char *pt = sm + oP + gr * 2 * kHalf, *tt = sm + oT + gr * 2 * kHalf;
     const float *beta_s = reinterpret_cast<const float *>(sm + oGate + gr * kGate);
-    const float *cum_s = beta_s + C;
+    const float *neg_s = beta_s + C;  // -c: the high words, then the low ones
 
     // the blocks of P and T above the diagonal stay zero
     for (int k = at; k < 4 * 32 * 4; k += kAux)
@@ -926,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // blocks of 32 columns, the diagonal one first, 16 columns at a time
       const int blk = q & 1, t = 32 * blk + lane;
       const bool isA = q < 2;
-      const float ct = cum_s[t], rowf = isA ? beta_s[t] : p.scale;
+      const float ch = -neg_s[t], cl = -neg_s[C + t], rowf = isA ? beta_s[t] : p.scale;
       // U and O2 of chunk i - 2 have read the T and P in this one's place (the
       // other warps write T behind a barrier with these)
       if (!isA && i >= 2) sy.wait(kFreeP + gr, (i / 2 - 1) & 1);
@@ -936,15 +959,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = diag ? blk : 0, c = part & 1;
         // columns kept
         const int last = t >= len ? 0 : (diag ? (isA ? lane : lane + 1) - 16 * c : 16);
-        const float *cs = cum_s + 32 * e + 16 * c;
+        const float *cs = neg_s + 32 * e + 16 * c;
         float v[16], f[16];
+        const auto diff = [&](float h0, float h1, float l0, float l1) {
+          return __fadd2_rn(__fadd2_rn(make_float2(ch, ch), make_float2(h0, h1)),
+                            __fadd2_rn(make_float2(cl, cl), make_float2(l0, l1)));
+        };
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
           const float4 x = *reinterpret_cast<const float4 *>(cs + j);
-          f[j] = ex2_mufu(ct - x.x);
-          f[j + 1] = ex2_mufu(ct - x.y);
-          f[j + 2] = ex2_mufu(ct - x.z);
-          f[j + 3] = ex2_mufu(ct - x.w);
+          const float4 y = *reinterpret_cast<const float4 *>(cs + C + j);
+          const float2 a = diff(x.x, x.y, y.x, y.y), b = diff(x.z, x.w, y.z, y.w);
+          f[j] = ex2_mufu(a.x);
+          f[j + 1] = ex2_mufu(a.y);
+          f[j + 2] = ex2_mufu(b.x);
+          f[j + 3] = ex2_mufu(b.y);
         }
         tmem_get16(tl + kColS + 32 * e + 16 * c, v);
 #pragma unroll

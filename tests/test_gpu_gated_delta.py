@@ -561,3 +561,39 @@ def test_even_sizes_at_odd_places():
         assert worst(y, want.double()) <= tol and worst(last, wl.double()) <= tol
     y, _ = sss.gated_delta_fwd(**dict(d, h0=state), last_state=state, return_last_state=True)
     assert worst(y, want.double()) <= tol and worst(state, wl.double()) <= tol
+
+
+def resets(L, every, size):
+    """Steps of weak decays (a factor of 0.95 to 1) with a hard one, whose
+    log2 is -size, now and then: dt for A = -1 without softplus, and where the
+    hard ones are."""
+    g = torch.Generator(device="cuda").manual_seed(L)
+    dt = 0.05 * torch.rand(L, generator=g, device="cuda")
+    at = torch.arange(every // 2, L, every, device="cuda")
+    dt[at] = size * math.log(2)
+    return dt.to(BF), at.tolist()
+
+
+@pytest.mark.parametrize("size", [46.0, 461.0, 2300.0, 2.3e5, 2.3e6, 1e9, 1e38, math.inf])
+@pytest.mark.parametrize("plan,L,every", [("recurrent", 128, 41), ("chunked", 128, 41),
+                                          ("chunked", 192, 7), ("auto", 1536, 111)])
+def test_weak_decays_after_a_hard_one(plan, L, every, size):
+    """A step that wipes the state (its decay is 0 in fp32 from log2 -150 on)
+    takes nothing from the precision of the decays after it, nor does one that
+    leaves next to nothing.  Every stretch between two of them and every head
+    is measured by its own largest value.  A running sum of log2 decays is off
+    by at most 2^-24 of the weak part and of what the sum's low word leaves,
+    2^-47 of 64 * 300: inside the (dstate + 16) half steps of fp32 that the
+    tolerance counts.  (auto: segments, as for those.)"""
+    d = delta_inputs(1, L, 2, 64, 1, 64, BF, h0=True)
+    dt, at = resets(L, every, size)
+    d["dt"] = dt[None, :, None].expand(1, L, 2)
+    d["A"], d["dt_bias"] = torch.tensor([-1.0, -0.75], device="cuda"), None
+    y, last = sss.gated_delta_fwd(**d, dt_softplus=False, plan=PLANS[plan],
+                                  return_last_state=True, check_status=True)
+    yr, lr = gated_delta(**d, dt_softplus=False)
+    tol = (3 if plan == "auto" else 1) * tolerance(64, L, F32, plan != "recurrent")
+    for h in range(2):
+        for lo, hi in zip([0] + at, at + [L]):
+            assert worst(y[0, lo:hi, h], yr[0, lo:hi, h]) <= tol, (h, lo)
+        assert worst(last[0, h], lr[0, h]) <= tol
