@@ -934,7 +934,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (len < C) {
         // keys and values of whatever lies behind the sequence: nothing of
         // them may enter a product over steps (zero times a NaN would)
+        // (these warps wait for V here alone: V of chunk i - 2 first, which may
+        // still be on its way, and while it is a wait for the phase after it
+        // would find the parity of the one before and pass; V of i - 4 is
+        // there, the gates of chunk i hang on the output of i - 3)
         sy.wait(kFullKQ + st, (i / 3) & 1);
+        if (i >= 2) sy.wait(kFullV + gr, (i / 2 - 1) & 1);
         sy.wait(kFullV + gr, (i / 2) & 1);
         const int rows = C - len;
         for (int k = at; k < rows * 32; k += kAux) {

@@ -597,3 +597,38 @@ def test_weak_decays_after_a_hard_one(plan, L, every, size):
         for lo, hi in zip([0] + at, at + [L]):
             assert worst(y[0, lo:hi, h], yr[0, lo:hi, h]) <= tol, (h, lo)
         assert worst(last[0, h], lr[0, h]) <= tol
+
+
+@pytest.mark.parametrize("chunks", [0, 1, 2, 3, 4])
+def test_tails_with_every_sm_busy(chunks):
+    """Last chunks of every length behind 0 to 4 whole ones, NaN behind each
+    sequence, more blocks than SMs and a copy beside them that keeps the memory
+    busy: what the tail clears of K and V is that chunk's own, so the bits are
+    those of the same rows with zeros behind them, in every run."""
+    tails = [1, 2, 15, 16, 17, 31, 32, 33, 48, 49, 62, 63]
+    lens = [64 * chunks + t for t in tails for _ in range(2)]
+    starts, at = [], 0
+    for n in lens:  # (in whole rows of 8 steps, some behind each)
+        starts += [at, at + n]
+        at += n + 8
+    cu = torch.tensor(starts + [at], dtype=torch.int32, device="cuda")
+    seqs = len(cu) - 1  # every other one is the rows behind a sequence
+    d = delta_inputs(1, at, 32, 128, 8, 128, BF, seed=chunks, h0=True, seqs=seqs)
+    keep = torch.zeros(at, dtype=torch.bool, device="cuda")
+    for lo, hi in zip(starts[::2], starts[1::2]):
+        keep[lo:hi] = True
+    def run(fill):
+        for n in ("q", "k", "v", "dt", "beta"):
+            d[n][:, ~keep] = fill
+        return sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=True, plan=2,
+                                   check_status=True)
+    want, wl = run(0.0)
+    big, other = torch.empty(2, 1 << 27, device="cuda"), torch.cuda.Stream()
+    for _ in range(4):
+        with torch.cuda.stream(other):
+            for _ in range(4):
+                big[1].copy_(big[0])
+        y, last = run(float("nan"))
+        assert torch.equal(y[:, keep], want[:, keep])
+        assert torch.equal(last[::2], wl[::2])
+    other.synchronize()
