@@ -934,12 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (len < C) {
         // keys and values of whatever lies behind the sequence: nothing of
         // them may enter a product over steps (zero times a NaN would)
-        // (these warps wait for V here alone: V of chunk i - 2 first, which may
-        // still be on its way, and while it is a wait for the phase after it
-        // would find the parity of the one before and pass; V of i - 4 is
-        // there, the gates of chunk i hang on the output of i - 3)
         sy.wait(kFullKQ + st, (i / 3) & 1);
-        if (i >= 2) sy.wait(kFullV + gr, (i / 2 - 1) & 1);
         sy.wait(kFullV + gr, (i / 2) & 1);
         const int rows = C - len;
         for (int k = at; k < rows * 32; k += kAux) {
@@ -1054,6 +1049,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       fence_async_smem();
+      // Where the group's next chunk is a tail, its wait for V there is for the
+      // phase after this chunk's V, which has to be over by then: with V of
+      // this chunk still on its way, the parity would be that of the phase
+      // before, and the wait would pass.  Here, before T is handed over, the V
+      // that is to come next cannot have been loaded yet, so this wait is sure
+      // of its phase; V is behind the product before, long before T is due.
+      if (i + 2 == nc - 1 && total < nc * C) sy.wait(kFullV + gr, (i / 2) & 1);
       warp_arrive(bar + kReadyT + gr, lane);
       if (lane == 0) mbar_arrive(bar + kFreeG + gr);
       // (the next chunk's A overwrites what the last product read)

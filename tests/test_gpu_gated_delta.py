@@ -632,3 +632,21 @@ def test_tails_with_every_sm_busy(chunks):
         assert torch.equal(y[:, keep], want[:, keep])
         assert torch.equal(last[::2], wl[::2])
     other.synchronize()
+
+
+def test_packed_calls_one_behind_the_other():
+    """Ragged packs of more blocks than SMs, hundreds of calls that nothing
+    waits between: none of their waits runs out, and the last call's bits are
+    the first's."""
+    cu = torch.tensor([0, 700, 700, 1362, 1363, 1500, 1890, 1999, 2600, 2663, 2999],
+                      dtype=torch.int32, device="cuda")
+    d = delta_inputs(1, 3002, 32, 128, 16, 128, BF, h0=True, seqs=10)
+    y = torch.zeros(1, 3002, 32, 128, device="cuda", dtype=BF)
+    last = torch.empty(10, 32, 128, 128, device="cuda")
+    kw = dict(cu_seqlens=cu, return_last_state=True, plan=2)
+    want, wl = (t.clone() for t in sss.gated_delta_fwd(**d, **kw, y=y, last_state=last,
+                                                       check_status=True))
+    for _ in range(600):
+        sss.gated_delta_fwd(**d, **kw, y=y, last_state=last)
+    assert sss.gated_delta_status() == sss.MSS_OK
+    assert torch.equal(y, want) and torch.equal(last, wl)
