@@ -66,8 +66,10 @@
  * by the caller, nothing allocated, work enqueued on `stream` without
  * synchronising; argument errors enqueue nothing.  Outputs must not overlap
  * inputs, except last_state = h0.  The chunked kernel's waits are bounded
- * (spin_timeout_ns, 0 = 2 s); one that runs out is recorded in a library
- * status word (one per device) read and cleared by mss_gated_delta_status().
+ * (spin_timeout_ns, 0 = 2 s; counted in tries of 4 us); one that runs out is
+ * recorded in a library status word (one per device) read and cleared by
+ * mss_gated_delta_status().  y and last_state are then not to be used.  Copies
+ * and products in flight are waited for all the same, for up to 2 s.
  */
 #ifndef SSS48_GATED_DELTA_H
 #define SSS48_GATED_DELTA_H

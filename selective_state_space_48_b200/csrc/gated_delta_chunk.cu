@@ -128,13 +128,15 @@ __device__ __forceinline__ int bar_count(int i) {
 // the instruction caches bound this kernel where every SM runs it (108 KB of
 // code took twice the time; 78 KB, with the products unrolled, 292 us for 8 x
 // 2048 steps, 71 KB, with them in loops, 275, though alone on its SMs the
-// longer form is 2 % faster).  A
-// wait gives up after `limit` tries, each of which suspends the thread for up
-// to kTryNs; then, and once any wait of the block has given up, every wait
-// that is not complete returns (the results are garbage, but nothing hangs:
-// products run on whatever their operands hold), and the block's end records
-// the timeout.
-constexpr uint32_t kTryNs = 20000;
+// longer form is 2 % faster).  A try suspends the thread for up to 4.0 us
+// (measured: hints of 1 ns to 1 ms gave the same), and a wait gives up after
+// `limit` of them (read off the clock instead, the limit made the kernel 2 to 3
+// % slower by its size).  Then, and once any wait of the block has given up,
+// every wait that is not complete returns after one try (the results are
+// garbage, but nothing hangs: products run on whatever their operands hold),
+// and the block's end records the timeout.
+constexpr uint32_t kTryNs = 4000;
+constexpr uint32_t kDrainTries = 2000000000u / kTryNs;  // 2 s
 struct Waits {
   uint32_t bar;  // shared-memory address of the barriers
   volatile int *abort;
@@ -170,12 +172,13 @@ struct Waits {
       if (++n >= limit) *abort = 1;
     } while (!try_wait(i, parity));
   }
-  // not cut short by another wait's timeout: for copies and products still in
-  // flight at the end
+  // for copies and products still in flight at the end, which no block may
+  // leave behind: neither cut short by another wait's timeout nor by a caller's
+  // short limit
   __device__ __forceinline__ void drain(int i, uint32_t parity) const {
     uint32_t n = 0;
     while (!try_wait(i, parity))
-      if (++n >= limit) {
+      if (++n >= kDrainTries) {
         *abort = 1;
         break;
       }

@@ -650,3 +650,32 @@ def test_packed_calls_one_behind_the_other():
         sss.gated_delta_fwd(**d, **kw, y=y, last_state=last)
     assert sss.gated_delta_status() == sss.MSS_OK
     assert torch.equal(y, want) and torch.equal(last, wl)
+
+
+@pytest.mark.parametrize("size,cu,out_dtype", [
+    ((1, 192, 2, 128, 1, 128), None, BF), ((4, 130, 32, 128, 8, 128), None, F32),
+    ((1, 2048, 1, 64, 1, 64), None, BF), ((1, 300, 4, 100, 2, 60), None, BF),
+    ((1, 264, 8, 64, 2, 64), [0, 70, 70, 71, 200, 264], BF)])
+def test_a_wait_that_runs_out_is_reported(size, cu, out_dtype):
+    """Waits of a microsecond (a chunk's inverse alone takes several) end the
+    call with a status, once, whatever it computes: whole sequences, segments,
+    copies, packed ones.  The calls after it are as before."""
+    seqs = None if cu is None else len(cu) - 1
+    cu = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    d = delta_inputs(*size, BF, h0=True, seqs=seqs)
+    kw = dict(cu_seqlens=cu, out_dtype=out_dtype, return_last_state=True)
+    want, wl = sss.gated_delta_fwd(**d, **kw, check_status=True)
+    y = torch.empty_like(want)
+    a = sss.make_gated_delta_args(**d, y=y, cu_seqlens=cu, spin_timeout_ns=1)
+    ws = torch.empty(max(workspace_bytes(a), 16), dtype=torch.uint8, device="cuda")
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+    for _ in range(3):
+        assert call(a) == sss.MSS_OK
+        assert sss.gated_delta_status() == sss.MSS_ERR_TIMEOUT
+        assert sss.gated_delta_status() == sss.MSS_OK
+    got, gl = sss.gated_delta_fwd(**d, **kw, check_status=True)
+    assert torch.equal(got, want) and torch.equal(gl, wl)
+    a.spin_timeout_ns = 10 ** 18  # (above what the kernel counts to)
+    assert call(a) == sss.MSS_OK
+    assert sss.gated_delta_status() == sss.MSS_OK
+    assert torch.equal(y, want)
