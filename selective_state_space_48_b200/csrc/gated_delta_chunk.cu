@@ -85,7 +85,7 @@ constexpr int kGate = 3 * C * 4;
 constexpr int oDecay = oGate + 2 * kGate;  // three of (2^(c_last - c), 2^c, scale 2^c) [C]
 constexpr int kDecay = 3 * C * 4;
 constexpr int oBar = oDecay + 3 * kDecay;
-constexpr int kBars = 36;
+constexpr int kBars = 37;
 constexpr int oTmemSlot = oBar + kBars * 8;
 constexpr int oAbort = oTmemSlot + 4;
 constexpr int oSeq = oAbort + 4;
@@ -105,7 +105,9 @@ constexpr uint32_t kTmemCols = 512;
 
 // Barriers.  Tiles landed and released; per chunk, products done (S, X, U, O1,
 // the update, O) and operands ready (H; R; U'; U; T and P), S and O drained; y
-// staged; the two P buffers released; the gates written (the decays have three
+// staged (two: nothing but time keeps the chain from staging a chunk's y before
+// the warp that stores it has looked for the one before); the two P buffers
+// released; the gates written (the decays have three
 // buffers, the rest two) and their two and three buffers released; every
 // product done.  A waiter may not fall two phases behind: where it could, the
 // barriers are a ring.  The groups arrive one lane per warp.  (H, R and U' in
@@ -113,14 +115,14 @@ constexpr uint32_t kTmemCols = 512;
 // waits than they gained: 618 us against 482 for 8192 steps.)
 constexpr int kFullKQ = 0, kFullV = 3, kEmptyKQ = 5, kEmptyV = 8, kDoneS = 9, kDoneX = 11,
               kDoneU = 12, kDoneO1 = 13, kDoneH = 14, kDoneO = 15, kReadyH = 16, kReadyR = 17,
-              kReadyU = 18, kReadyO = 19, kFreeO = 20, kReadyY = 21, kFreeS = 22, kReadyT = 23,
-              kFreeP = 25, kReadyG = 27, kFreeG = 30, kFreeD = 32,
-              kEnd = 35;
+              kReadyU = 18, kReadyO = 19, kFreeO = 20, kReadyY = 21, kFreeS = 23, kReadyT = 24,
+              kFreeP = 26, kReadyG = 28, kFreeG = 31, kFreeD = 33,
+              kEnd = 36;
 // arrivals that complete a barrier's phase
 __device__ __forceinline__ int bar_count(int i) {
   if (i == kFreeS || i == kReadyT || i == kReadyT + 1 || i == kFreeG || i == kFreeG + 1)
     return kAuxWarps;
-  if ((i >= kReadyH && i <= kReadyY) || (i >= kFreeD && i < kEnd)) return kChainWarps;
+  if ((i >= kReadyH && i <= kReadyY + 1) || (i >= kFreeD && i < kEnd)) return kChainWarps;
   return 1;
 }
 
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (i == 0 || !y_tma || i * C > total) continue;
         // y of chunk i - 1, a whole one, staged in its Q tile; then the stage
         // is free
-        sy.wait(kReadyY, (i - 1) & 1);
+        sy.wait(kReadyY + ((i - 1) & 1), ((i - 1) / 2) & 1);
         const int t = static_cast<int>(t0) + (i - 1) * C, a = (i - 1) % 3;
         const unsigned char *y = sm + oKQ + a * kStageKQ + kHalf;
         if (write_y && !*abort) {
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<OutT *>(d + (ycol ^ ((j & 7) << 4)) + j * 128) = from_f32<OutT>(o[j]);
           fence_async_smem();
         }
-        warp_arrive(bar + kReadyY, lane);
+        warp_arrive(bar + kReadyY + (i & 1), lane);
       } else if (write_y && row < P) {
         OutT *yr = yp + static_cast<int64_t>(i * C + 16 * e) * p.sy[1];
 #pragma unroll
