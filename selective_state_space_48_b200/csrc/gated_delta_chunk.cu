@@ -1146,6 +1146,8 @@ __global__ void __launch_bounds__(256) delta_join_kernel(const DeltaParams p) {
 
 // Copies of q, k, v (blockIdx.y) whose rows start on 16 bytes, for sizes and
 // views that tensor maps do not take: a warp four rows, two channels of a lane.
+// Rows end in zeros up to the next 16 bytes: a map's width then cuts inside
+// them, and what is behind it is 0 whether the copy engine cuts there or not.
 constexpr int kCopyWarps = 8, kCopyRows = 4;
 __global__ void __launch_bounds__(32 * kCopyWarps)
     delta_copy_kernel(const __grid_constant__ DeltaParams p, __nv_bfloat16 *q, __nv_bfloat16 *k,
@@ -1166,11 +1168,11 @@ __global__ void __launch_bounds__(32 * kCopyWarps)
       const int64_t r = r0 + i < rows ? r0 + i : rows - 1, t = r / heads, b = t / p.L;
       from[i] = src + b * st[0] + (t - b * p.L) * st[1] + (r - t * heads) * st[2];
     }
-    for (int64_t c = 2 * lane; c < width; c += 64) {
+    for (int64_t c = 2 * lane; c < pitch; c += 64) {
       __nv_bfloat162 two[kCopyRows];
 #pragma unroll
       for (int i = 0; i < kCopyRows; ++i) {
-        two[i].x = from[i][c];
+        two[i].x = c < width ? from[i][c] : __float2bfloat16(0.f);
         two[i].y = c + 1 < width ? from[i][c + 1] : __float2bfloat16(0.f);
       }
 #pragma unroll

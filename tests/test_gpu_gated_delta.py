@@ -679,3 +679,26 @@ def test_a_wait_that_runs_out_is_reported(size, cu, out_dtype):
     assert call(a) == sss.MSS_OK
     assert sss.gated_delta_status() == sss.MSS_OK
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("size", ODD_SIZES + [(2, 100, 2, 57, 1, 121)])
+def test_copies_read_nothing_behind_their_rows(size):
+    """A workspace full of NaN gives the bits of one full of zeros, and the
+    copies' rows end in zeros."""
+    B, L, H, P, G, N = size
+    d = delta_inputs(*size, BF, h0=True)
+    y, last = torch.empty_like(d["v"]), torch.empty(B, H, P, N, device="cuda")
+    a = sss.make_gated_delta_args(**d, y=y, last_state=last)
+    n = workspace_bytes(a)
+    got = []
+    for fill in (0, 255):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        a.workspace, a.workspace_bytes = ws.data_ptr(), n
+        assert call(a) == sss.MSS_OK
+        assert sss.gated_delta_status() == sss.MSS_OK
+        got.append((y.clone(), last.clone()))
+        width, pitch = (N, -(-N // 8) * 8)
+        rows = ws[:2 * B * L * G * pitch].view(BF).view(-1, pitch)
+        assert torch.equal(rows[:, :width], d["q"].reshape(-1, N))
+        assert (rows[:, width:] == 0).all()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
