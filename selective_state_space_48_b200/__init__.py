@@ -793,22 +793,25 @@ def _check_views(device, named):
             raise ValueError(f"{name} must have a contiguous last dimension")
 
 
-class _on_device:
-    """The call's device as the current one while its kernels are enqueued,
-    and the stream: the caller's, or that device's current one."""
-
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self._guard = torch.cuda.device(device)
-        self._device, self._stream = device, stream
-
-    def __enter__(self):
-        self._guard.__enter__()
-        return self._stream or torch.cuda.current_stream(self._device)
-
-    def __exit__(self, *exc):
-        self._guard.__exit__(*exc)
+def _under(stream, like, call, *args, **kw):
+    """``call`` with ``stream`` as the current one.  What it allocates is then
+    that stream's own memory, in that stream's order: from the current
+    stream's, it could be a block that its kernels still read or write.  The
+    results are recorded on the caller's stream, which is to use and drop
+    them."""
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        return call(*args, **kw)  # refuses them
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
+    caller = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    if caller != stream:
+        outs = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else [out]
+        for t in outs:
+            if t is not None:
+                t.record_stream(caller)
+    return out
 
 
 # The calls below fill their argument structs with one struct.pack and look
@@ -844,12 +847,13 @@ def _entry(name):
     return fn
 
 
-def _enqueue(name, packed, device, stream):
-    if stream is None and torch._C._cuda_getDevice() == device.index:
+def _enqueue(name, packed, device):
+    """On the device's current stream, with the device as the current one."""
+    if torch._C._cuda_getDevice() == device.index:
         rc = _entry(name)(packed, torch._C._cuda_getCurrentRawStream(device.index))
     else:
-        with _on_device(device, stream) as s:
-            rc = _entry(name)(packed, s.cuda_stream)
+        with torch.cuda.device(device):
+            rc = _entry(name)(packed, torch._C._cuda_getCurrentRawStream(device.index))
     if rc != MSS_OK:
         raise MssError(rc, name)
 
@@ -925,14 +929,10 @@ def _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scal
         int(spin_timeout_ns), *workspace)
 
 
-def _workspace(nbytes, device, stream):
-    """The workspace of a call; on the caller's own stream it is kept
-    until that stream has used it (on the current one the allocator does)."""
+def _workspace(nbytes, device):
     if not nbytes:
         return None, 0
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
     return ws, ws.data_ptr()
 
 
@@ -992,6 +992,10 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
     ``out_dtype`` (and the final states when ``return_last_state``).  Forward
     only: no gradients pass.
     """
+    if stream is not None:
+        return _under(stream, q, gated_delta_fwd, q, k, v, dt, A, beta, dt_bias, dt_softplus,
+                      beta_sigmoid, scale, h0, return_last_state, out_dtype, y, last_state,
+                      cu_seqlens, None, check_status, plan)
     if not isinstance(v, _Tensor) or not isinstance(q, _Tensor):
         raise TypeError("q and v must be CUDA tensors")
     if v.dim() != 4 or q.dim() != 4:
@@ -1016,12 +1020,12 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
         else:
             nbytes = _delta_room(DeltaArgs.from_buffer_copy(_pack_delta(*values)), v.device.index)
         if nbytes:
-            ws, pws = _workspace(nbytes, v.device, stream)
+            ws, pws = _workspace(nbytes, v.device)
             values = (*values[:-2], pws, nbytes)
-    _enqueue("gated_delta_fwd", _pack_delta(*values), q.device, stream)
+    _enqueue("gated_delta_fwd", _pack_delta(*values), q.device)
     if check_status:
-        with _on_device(q.device, stream) as s:
-            rc = load_library().mss_gated_delta_status(_stream_handle(s))
+        with torch.cuda.device(q.device):
+            rc = gated_delta_status()
         if rc != MSS_OK:
             raise MssError(rc, "mss_gated_delta_status")
     return (y, last_state) if return_last_state else y
@@ -1040,6 +1044,9 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
     nheads, headdim, dstate) float32 is updated in place.  q, k: (batch,
     ngroups, dstate); v: (batch, nheads, headdim); dt, beta: (batch, nheads);
     views as for ``gated_delta_fwd``.  Returns y (batch, nheads, headdim)."""
+    if stream is not None:
+        return _under(stream, q, gated_delta_update, state, q, k, v, dt, A, beta, dt_bias,
+                      dt_softplus, beta_sigmoid, scale, out_dtype, y)
     if not _tensors(state, q, v, state):
         raise TypeError("state, q and v must be CUDA tensors")
     if state.dim() != 4 or q.dim() != 3:
@@ -1069,7 +1076,7 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
         0 if dt_bias is None else dt_bias.data_ptr(), bool(dt_softplus), bool(beta_sigmoid),
         N ** -0.5 if scale is None else float(scale), y.data_ptr(), *q.stride()[:2],
         *k.stride()[:2], *v.stride()[:2], *dt.stride(), *beta.stride(), *y.stride()[:2])
-    _enqueue("gated_delta_update", packed, dev, stream)
+    _enqueue("gated_delta_update", packed, dev)
     return y
 
 
@@ -1162,6 +1169,9 @@ def gated_rmsnorm_fwd(x, z, weight, eps=1e-5, group_size=None, norm_before_gate=
     ``group_size`` channels (default: the width), of x o silu(z), or of x
     with the gate applied after it (``norm_before_gate``).  Returns y like x.
     """
+    if stream is not None:
+        return _under(stream, x, gated_rmsnorm_fwd, x, z, weight, eps, group_size,
+                      norm_before_gate, y)
     rows, width, gs, shared = _gated_norm_sizes(x, weight, group_size)
     dev, kind, shape = x.device, x.dtype, x.shape
     if y is None:
@@ -1170,7 +1180,7 @@ def gated_rmsnorm_fwd(x, z, weight, eps=1e-5, group_size=None, norm_before_gate=
                                                          ("y", y, kind)))
     _enqueue("gated_rmsnorm_fwd", _pack_gated_norm(
         rows, width, gs, _dtype_code(kind), bool(norm_before_gate), shared, eps, px, pz,
-        weight.data_ptr(), py, 0, 0, 0, 0, sx, sz, sy, 0, 0, 0, 0, 0), dev, stream)
+        weight.data_ptr(), py, 0, 0, 0, 0, sx, sz, sy, 0, 0, 0, 0, 0), dev)
     return y
 
 
@@ -1179,6 +1189,9 @@ def gated_rmsnorm_bwd(x, z, weight, dy, eps=1e-5, group_size=None, norm_before_g
     """Gradients of sum(dy * y) for ``gated_rmsnorm_fwd`` on the same inputs.
     Returns a dict of dx, dz (x's dtype) and dweight (float32, like weight,
     None unless ``need_dweight``)."""
+    if stream is not None:
+        return _under(stream, x, gated_rmsnorm_bwd, x, z, weight, dy, eps, group_size,
+                      norm_before_gate, need_dweight)
     rows, width, gs, shared = _gated_norm_sizes(x, weight, group_size)
     dev, kind, shape = x.device, x.dtype, x.shape
     dx, dz = _new(x), _new(x)
@@ -1186,11 +1199,11 @@ def gated_rmsnorm_bwd(x, z, weight, dy, eps=1e-5, group_size=None, norm_before_g
     (px, pz, pdy, pdx, pdz), (sx, sz, sdy, sdx, sdz) = _norm_rows(dev, shape, (
         ("x", x, kind), ("z", z, kind), ("dy", dy, kind), ("dx", dx, kind), ("dz", dz, kind)))
     nbytes = _norm_workspace_bytes("gated", rows, width, gs, 1, dev.index) if need_dweight else 0
-    ws, pws = _workspace(nbytes, dev, stream)
+    ws, pws = _workspace(nbytes, dev)
     _enqueue("gated_rmsnorm_bwd", _pack_gated_norm(
         rows, width, gs, _dtype_code(kind), bool(norm_before_gate), shared, eps, px, pz,
         weight.data_ptr(), 0, pdy, pdx, pdz, dw.data_ptr() if need_dweight else 0, sx, sz, 0, sdy,
-        sdx, sdz, pws, nbytes), dev, stream)
+        sdx, sdz, pws, nbytes), dev)
     return {"dx": dx, "dz": dz, "dweight": dw}
 
 
@@ -1218,6 +1231,9 @@ def add_rmsnorm_fwd(x, residual, weight, scale=None, eps=1e-5, residual_dtype=No
     (width,) float32.  ``residual_out`` may be the residual itself.  Returns
     (y in x's dtype, r in the residual's dtype).
     """
+    if stream is not None:
+        return _under(stream, x, add_rmsnorm_fwd, x, residual, weight, scale, eps,
+                      residual_dtype, y, residual_out)
     rows, width = _add_norm_sizes(x, weight, scale)
     dev, kind, shape = x.device, x.dtype, x.shape
     if residual_out is None:
@@ -1232,7 +1248,7 @@ def add_rmsnorm_fwd(x, residual, weight, scale=None, eps=1e-5, residual_dtype=No
     _enqueue("add_rmsnorm_fwd", _pack_add_norm(
         rows, width, _dtype_code(kind), _dtype_code(rd), eps, px, pr,
         0 if scale is None else scale.data_ptr(), weight.data_ptr(), py, po, 0, 0, 0, 0, 0, 0,
-        sx, sr, sy, so, 0, 0, 0, 0, 0, 0), dev, stream)
+        sx, sr, sy, so, 0, 0, 0, 0, 0, 0), dev)
     return y, residual_out
 
 
@@ -1243,6 +1259,9 @@ def add_rmsnorm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, scale=
     dscale only.  Returns a dict of dx (dy's dtype), dresidual (the
     residual's dtype), dweight and dscale (float32; None where not asked for
     or there is no scale)."""
+    if stream is not None:
+        return _under(stream, residual_out, add_rmsnorm_bwd, residual_out, weight, dy,
+                      dresidual_out, x, scale, eps, need_dweight, need_dscale)
     rows, width = _add_norm_sizes(residual_out, weight, scale)
     if not isinstance(dy, torch.Tensor):
         raise TypeError("dy must be a CUDA tensor")
@@ -1258,12 +1277,12 @@ def add_rmsnorm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, scale=
         ("x", x if need_dscale else None, kind), ("dx", dx, kind), ("dresidual", dres, rd)))
     sums = (1 if need_dweight else 0) + (2 if need_dscale else 0)
     nbytes = _norm_workspace_bytes("add", rows, width, 0, sums, dev.index) if sums else 0
-    ws, pws = _workspace(nbytes, dev, stream)
+    ws, pws = _workspace(nbytes, dev)
     _enqueue("add_rmsnorm_bwd", _pack_add_norm(
         rows, width, _dtype_code(kind), _dtype_code(rd), eps, px, 0,
         0 if scale is None else scale.data_ptr(), weight.data_ptr(), 0, po, pdy, pdo, pdx, pdr,
         dw.data_ptr() if need_dweight else 0, ds.data_ptr() if need_dscale else 0,
-        sx, 0, 0, so, sdy, sdo, sdx, sdr, pws, nbytes), dev, stream)
+        sx, 0, 0, so, sdy, sdo, sdx, sdr, pws, nbytes), dev)
     return {"dx": dx, "dresidual": dres, "dweight": dw, "dscale": ds}
 
 

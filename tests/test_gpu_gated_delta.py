@@ -702,3 +702,68 @@ def test_copies_read_nothing_behind_their_rows(size):
         assert torch.equal(rows[:, :width], d["q"].reshape(-1, N))
         assert (rows[:, width:] == 0).all()
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def delayed(stream, ms=20):
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(int(ms * 2e6))
+
+
+def stream_calls():
+    """Calls of every operator (taking a stream) with the bytes of what each
+    allocates."""
+    d = delta_inputs(2, 100, 4, 64, 2, 64, BF, h0=True)
+    seg = delta_inputs(1, 1500, 2, 64, 1, 64, BF)
+    ws = workspace_bytes(sss.make_gated_delta_args(**seg))
+    one = {n: (t[:, 0] if n in ("q", "k", "v", "dt", "beta") else t)
+           for n, t in d.items() if n != "h0"}
+    x, z = torch.randn(2, 64, 512, device="cuda")
+    w = torch.ones(512, device="cuda")
+    y = torch.empty(1, 1500, 2, 64, device="cuda")
+    size = 4 * x.numel()
+
+    def update(s):
+        with torch.cuda.stream(s or torch.cuda.current_stream()):
+            state = d["h0"].clone()  # (in that stream's order)
+        return sss.gated_delta_update(state, **one, stream=s)
+
+    return {
+        "fwd": (lambda s: sss.gated_delta_fwd(**d, stream=s), 4 * d["v"].numel()),
+        "fwd state": (lambda s: sss.gated_delta_fwd(**d, return_last_state=True, stream=s)[1],
+                      4 * d["h0"].numel()),
+        "workspace": (lambda s: sss.gated_delta_fwd(**seg, y=y, stream=s), ws),
+        "update": (update, 4 * one["v"].numel()),
+        "gated": (lambda s: sss.gated_rmsnorm_fwd(x, z, w, stream=s), size),
+        "gated bwd": (lambda s: sss.gated_rmsnorm_bwd(x, z, w, z, stream=s)["dz"], size),
+        "add": (lambda s: sss.add_rmsnorm_fwd(x, z, w, stream=s)[0], size),
+        "add bwd": (lambda s: sss.add_rmsnorm_bwd(x, w, z, stream=s)["dx"], size),
+    }
+
+
+@pytest.mark.parametrize("name", ["fwd", "fwd state", "workspace", "update", "gated", "gated bwd",
+                                  "add", "add bwd"])
+def test_streams_do_not_share_memory(name):
+    """A call on a stream of its own allocates nothing that the current
+    stream has freed and still uses, and what it still writes is not handed to
+    the current stream when it is dropped."""
+    call, nbytes = stream_calls()[name]
+    want = call(None).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    # blocks of that size, freed while the current stream has yet to read them
+    held = [torch.full((nbytes // 4,), 5.0, device="cuda") for _ in range(8)]
+    delayed(torch.cuda.current_stream())
+    sums = [t.sum(dtype=torch.float64) for t in held]
+    del held
+    out = call(side)
+    torch.cuda.synchronize()
+    assert [float(v) for v in sums] == [5.0 * (nbytes // 4)] * 8
+    assert torch.equal(out, want)
+    del out
+    # dropped while that stream has yet to write it
+    delayed(side)
+    call(side)
+    held = [torch.full((nbytes // 4,), 5.0, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(bool((t == 5).all()) for t in held)
