@@ -376,6 +376,27 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _under(stream, like, call, *args, **kw):
+    """``call`` with ``stream`` as the current one.  What it allocates is then
+    that stream's own memory, in that stream's order: from the current
+    stream's, it could be a block that its kernels still read or write.  The
+    results are recorded on the caller's stream, which is to use and drop
+    them."""
+    if not isinstance(like, torch.Tensor) or not like.is_cuda:
+        return call(*args, **kw)  # refuses them
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
+    caller = torch.cuda.current_stream(like.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    if caller != stream:
+        outs = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else [out]
+        for t in outs:
+            if t is not None:
+                t.record_stream(caller)
+    return out
+
+
 def make_scan_args(u, delta, A, B, C, D=None, z=None, delta_bias=None,
                    delta_softplus=True, h0=None, y=None, last_state=None,
                    workspace=None, plan_splits=0, test_flags=0,
@@ -462,6 +483,11 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None,
     y (batch, dim, L) in ``out_dtype`` (and the final state when
     ``return_last_state``).
     """
+    if stream is not None:
+        return _under(stream, u, selective_scan_fwd, u, delta, A, B, C, D, z, delta_bias,
+                      delta_softplus, h0, return_last_state, out_dtype, y, last_state, workspace,
+                      None, plan_splits, test_flags, spin_timeout_ns, check_status, cu_seqlens,
+                      trapezoid, checkpoints)
     batch, dim, L = u.shape
     N = A.shape[1]
     if y is None:
@@ -478,16 +504,16 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None,
         args.workspace = workspace.data_ptr()
         args.workspace_bytes = workspace.numel() * workspace.element_size()
     lib = load_library()
-    rc = lib.mamba_selective_scan_fwd(ctypes.byref(args), _stream_handle(stream))
+    rc = lib.mamba_selective_scan_fwd(ctypes.byref(args), _stream_handle(None))
     if rc != MSS_OK:
         raise MssError(rc, "mamba_selective_scan_fwd")
     if check_status:
-        rc = lib.mss_scan_status(ctypes.byref(args), _stream_handle(stream))
+        rc = lib.mss_scan_status(ctypes.byref(args), _stream_handle(None))
         if rc != MSS_OK:
             raise MssError(rc, "mss_scan_status")
     # keep the workspace alive until the stream has used it
     if workspace is not None:
-        workspace.record_stream(stream or torch.cuda.current_stream())
+        workspace.record_stream(torch.cuda.current_stream())
     return (y, last_state) if return_last_state else y
 
 
@@ -502,6 +528,9 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
     """One decode step through ``selective_state_update``; ``state``
     (batch, dim, N) float32 is updated in place.  x, dt, z: (batch, dim);
     B, C: (batch, N).  Returns y (batch, dim)."""
+    if stream is not None:
+        return _under(stream, state, selective_state_update, state, x, dt, A, B, C, D, z, dt_bias,
+                      dt_softplus, out_dtype, y)
     batch, dim, N = state.shape
     ind = x.dtype
     _check_cuda("state", state, torch.float32)
@@ -524,7 +553,7 @@ def selective_state_update(state, x, dt, A, B, C, D=None, z=None, dt_bias=None,
     a.dt_bias = _ptr(dt_bias)
     a.dt_softplus = 1 if dt_softplus else 0
     a.y = _ptr(y)
-    rc = load_library().selective_state_update(ctypes.byref(a), _stream_handle(stream))
+    rc = load_library().selective_state_update(ctypes.byref(a), _stream_handle(None))
     if rc != MSS_OK:
         raise MssError(rc, "selective_state_update")
     return y
@@ -582,6 +611,9 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, h0=N
     ``ssd_workspace_size`` asks for; False runs every sequence whole; a
     uint8 CUDA tensor is used as given.
     """
+    if stream is not None:
+        return _under(stream, x, ssd_fwd, x, dt, A, B, C, D, z, dt_bias, dt_softplus, h0,
+                      return_last_state, out_dtype, y, last_state, None, check_status, workspace)
     batch, L, H, P = x.shape
     N = B.shape[3]
     if y is None:
@@ -595,14 +627,14 @@ def ssd_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=True, h0=N
         args.workspace = workspace.data_ptr()
         args.workspace_bytes = workspace.numel() * workspace.element_size()
     lib = load_library()
-    rc = lib.mamba2_ssd_fwd(ctypes.byref(args), _stream_handle(stream))
+    rc = lib.mamba2_ssd_fwd(ctypes.byref(args), _stream_handle(None))
     if rc != MSS_OK:
         raise MssError(rc, "mamba2_ssd_fwd")
     # keep the workspace alive until the stream has used it
     if workspace is not None and workspace is not False:
-        workspace.record_stream(stream or torch.cuda.current_stream())
+        workspace.record_stream(torch.cuda.current_stream())
     if check_status:
-        rc = lib.mss_ssd_status(_stream_handle(stream))
+        rc = lib.mss_ssd_status(_stream_handle(None))
         if rc != MSS_OK:
             raise MssError(rc, "mss_ssd_status")
     return (y, last_state) if return_last_state else y
@@ -641,6 +673,9 @@ def selective_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None,
     tensor is used as given.  Returns a dict of float32 tensors du, ddelta,
     dA, dB, dC, dD, dz, ddelta_bias, dh0 (None for absent inputs).
     """
+    if stream is not None:
+        return _under(stream, u, selective_scan_bwd, u, delta, A, B, C, dy, D, z, delta_bias,
+                      delta_softplus, h0, d_last, None, workspace, checkpoints, cu_seqlens)
     batch, dim, L = u.shape
     N = A.shape[1]
     ind = u.dtype
@@ -701,11 +736,11 @@ def selective_scan_bwd(u, delta, A, B, C, dy, D=None, z=None, delta_bias=None,
     if workspace is not None:
         a.workspace = workspace.data_ptr()
         a.workspace_bytes = workspace.numel() * workspace.element_size()
-    rc = lib.mamba_selective_scan_bwd(ctypes.byref(a), _stream_handle(stream))
+    rc = lib.mamba_selective_scan_bwd(ctypes.byref(a), _stream_handle(None))
     if rc != MSS_OK:
         raise MssError(rc, "mamba_selective_scan_bwd")
     if workspace is not None:
-        workspace.record_stream(stream or torch.cuda.current_stream())
+        workspace.record_stream(torch.cuda.current_stream())
     return g
 
 
@@ -791,27 +826,6 @@ def _check_views(device, named):
             raise ValueError(f"{name} must be contiguous")
         if inner == "rows" and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise ValueError(f"{name} must have a contiguous last dimension")
-
-
-def _under(stream, like, call, *args, **kw):
-    """``call`` with ``stream`` as the current one.  What it allocates is then
-    that stream's own memory, in that stream's order: from the current
-    stream's, it could be a block that its kernels still read or write.  The
-    results are recorded on the caller's stream, which is to use and drop
-    them."""
-    if not isinstance(like, torch.Tensor) or not like.is_cuda:
-        return call(*args, **kw)  # refuses them
-    if stream.device != like.device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {like.device}")
-    caller = torch.cuda.current_stream(like.device)
-    with torch.cuda.stream(stream):
-        out = call(*args, **kw)
-    if caller != stream:
-        outs = out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else [out]
-        for t in outs:
-            if t is not None:
-                t.record_stream(caller)
-    return out
 
 
 # The calls below fill their argument structs with one struct.pack and look
