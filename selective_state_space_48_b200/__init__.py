@@ -756,6 +756,34 @@ def scan_checkpoints(batch, dim, dstate, seqlen, device):
                        device=device)
 
 
+class _NoSecond(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, t, *sources):
+        return t.view_as(t)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the backward passes of selective_scan_fn, gated_rmsnorm_fn and "
+                           "add_rmsnorm_fn cannot be differentiated again")
+
+
+def _first_order(backward):
+    """A backward whose gradients raise when they are differentiated: they
+    hang on every tensor they were computed from.  (With torch's
+    once_differentiable they hang on nothing when the upstream gradient is a
+    constant, and a gradient penalty misses them without a word.)"""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        saved = ctx.saved_tensors  # (once: checkpointing allows no more)
+        with torch.no_grad():
+            out = backward(ctx, saved, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        sources = [t for t in (*saved, *grads) if t is not None and t.requires_grad]
+        return tuple(None if t is None else _NoSecond.apply(t, *sources) for t in out)
+    return run
+
+
 class _SelectiveScanFn(torch.autograd.Function):
     """Autograd wrapper: forward through mamba_selective_scan_fwd (writing
     the backward's state checkpoints), backward through
@@ -775,8 +803,9 @@ class _SelectiveScanFn(torch.autograd.Function):
         return y
 
     @staticmethod
-    def backward(ctx, dy):
-        u, delta, A, B, C, D, z, delta_bias, h0, ck, cu = ctx.saved_tensors
+    @_first_order
+    def backward(ctx, saved, dy):
+        u, delta, A, B, C, D, z, delta_bias, h0, ck, cu = saved
         g = selective_scan_bwd(u, delta, A, B, C, _rows_view(dy.float()), D=D, z=z,
                                delta_bias=delta_bias, delta_softplus=ctx.delta_softplus,
                                h0=h0, checkpoints=ck, cu_seqlens=cu)
@@ -1319,8 +1348,9 @@ class _GatedRmsNormFn(torch.autograd.Function):
         return gated_rmsnorm_fwd(x, z, weight, **ctx.kw)
 
     @staticmethod
-    def backward(ctx, dy):
-        x, z, weight = ctx.saved_tensors
+    @_first_order
+    def backward(ctx, saved, dy):
+        x, z, weight = saved
         g = gated_rmsnorm_bwd(x, z, weight, _even_rows(dy), need_dweight=ctx.needs_input_grad[2],
                               **ctx.kw)
         return g["dx"], g["dz"], g["dweight"], None, None, None
@@ -1345,8 +1375,9 @@ class _AddRmsNormFn(torch.autograd.Function):
         return y, res
 
     @staticmethod
-    def backward(ctx, dy, dres):
-        x, weight, scale, res = ctx.saved_tensors
+    @_first_order
+    def backward(ctx, saved, dy, dres):
+        x, weight, scale, res = saved
         if dy is None:
             dy = torch.zeros(res.shape, dtype=ctx.x_dtype, device=res.device)
         g = add_rmsnorm_bwd(res, weight, _even_rows(dy),

@@ -299,3 +299,29 @@ def test_parameters_as_weights():
     want = gated_rmsnorm(rmsnorm(total, lw, 1e-5), total, lw, 1e-5, 64, False).sum()
     for a, b in zip((dx, dw, ds), torch.autograd.grad(want, (lx, lw, ls))):
         assert worst(a, b) <= 4 * tol(64, F32, 3)
+
+
+@pytest.mark.parametrize("upstream", ["constant", "differentiable"])
+@pytest.mark.parametrize("op", ["gated", "add", "scan"])
+def test_second_derivatives_are_refused(op, upstream):
+    """create_graph gives the first derivative; differentiating that raises,
+    beside a path that has a second one and whatever the upstream gradient."""
+    r = rnd(3)
+    x, z, w = r(4, 64).requires_grad_(), r(4, 64), torch.ones(64, device="cuda")
+    if op == "scan":
+        y = sss.selective_scan_fn(x[None], z[None], -torch.ones(4, 8, device="cuda"),
+                                  r(1, 8, 64), r(1, 8, 64))[0]
+    else:
+        y = sss.gated_rmsnorm_fn(x, z, w) if op == "gated" else sss.add_rmsnorm_fn(x, z, w)[0]
+    loss = (y * x if upstream == "differentiable" else y).sum() + (x ** 3).sum()
+    first, = torch.autograd.grad(loss, x, create_graph=True)
+    plain, = torch.autograd.grad((y * x.detach() if upstream == "differentiable" else y).sum(), x,
+                                 retain_graph=True)
+    extra = y if upstream == "differentiable" else torch.zeros_like(x)
+    # three fp32 terms, added in either order: two roundings of a partial sum on
+    # each side, and up to four of the product 3 x^2, half a step of the terms'
+    # sizes each (the terms may cancel)
+    sizes = plain.abs() + extra.abs() + 3 * x ** 2
+    assert ((first - (plain + extra + 3 * x ** 2)).abs() <= 8 * U * sizes).all()
+    with pytest.raises(RuntimeError, match="differentiated again"):
+        torch.autograd.grad(first.sum(), x)
