@@ -923,6 +923,14 @@ def _new(like, dtype=None):
     return torch.empty(like.shape, dtype=dtype, device=like.device)
 
 
+def _refuse_gradients(call, *inputs):
+    """Raises where a gradient would be expected of a forward-only call."""
+    for t in inputs:
+        if t is not None and t.requires_grad:
+            raise RuntimeError(f"{call} is forward only and an input requires a gradient: detach "
+                               "it, or call under torch.no_grad()")
+
+
 def _same(t, dtype, device, shape):
     return (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device
             and t.shape == shape)
@@ -1033,7 +1041,8 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
     written.  h0 and last_state: (sequences, nheads, headdim, dstate)
     float32, and may be one tensor.  Returns y (batch, L, nheads, headdim) in
     ``out_dtype`` (and the final states when ``return_last_state``).  Forward
-    only: no gradients pass.
+    only: an input that requires a gradient is refused outside of
+    ``torch.no_grad()``.
     """
     if stream is not None:
         return _under(stream, q, gated_delta_fwd, q, k, v, dt, A, beta, dt_bias, dt_softplus,
@@ -1051,6 +1060,8 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
                                  dtype=torch.float32, device=v.device)
     values = _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y,
                            last_state, cu_seqlens, plan, 0, (0, 0))
+    if torch.is_grad_enabled():
+        _refuse_gradients("gated_delta_fwd", q, k, v, dt, A, beta, dt_bias, h0)
     ws = None
     if v.dtype is torch.bfloat16 and plan != MSS_DELTA_RECURRENT:
         at = q.data_ptr() | k.data_ptr() | v.data_ptr()
@@ -1086,7 +1097,8 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
     """One decode step through ``gated_delta_update``; ``state`` (batch,
     nheads, headdim, dstate) float32 is updated in place.  q, k: (batch,
     ngroups, dstate); v: (batch, nheads, headdim); dt, beta: (batch, nheads);
-    views as for ``gated_delta_fwd``.  Returns y (batch, nheads, headdim)."""
+    views, and inputs that require gradients, as for ``gated_delta_fwd``.
+    Returns y (batch, nheads, headdim)."""
     if stream is not None:
         return _under(stream, q, gated_delta_update, state, q, k, v, dt, A, beta, dt_bias,
                       dt_softplus, beta_sigmoid, scale, out_dtype, y)
@@ -1113,6 +1125,8 @@ def gated_delta_update(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus=Tr
             ("dt", dt, ind, heads, None), ("beta", beta, ind, heads, None),
             ("A", A, f32, (H,), "dense"), ("dt_bias", dt_bias, f32, (H,), "dense"),
             ("y", y, None, values, "rows")])
+    if torch.is_grad_enabled():
+        _refuse_gradients("gated_delta_update", state, q, k, v, dt, A, beta, dt_bias)
     packed = _pack_update(
         batch, H, P, G, N, _dtype_code(ind), _dtype_code(y.dtype), state.data_ptr(),
         q.data_ptr(), k.data_ptr(), v.data_ptr(), dt.data_ptr(), A.data_ptr(), beta.data_ptr(),

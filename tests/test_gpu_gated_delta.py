@@ -767,3 +767,21 @@ def test_streams_do_not_share_memory(name):
     held = [torch.full((nbytes // 4,), 5.0, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     assert all(bool((t == 5).all()) for t in held)
+
+
+@pytest.mark.parametrize("n", ["q", "k", "v", "dt", "A", "beta", "dt_bias", "h0"])
+def test_inputs_that_require_gradients_are_refused(n):
+    """The delta rule is forward only: no call returns values without the
+    graph that a gradient would need.  Under no_grad, and detached, it runs."""
+    d = delta_inputs(1, 70, 2, 64, 1, 64, F32, h0=True)
+    want = sss.gated_delta_fwd(**d)
+    d[n] = d[n].clone().requires_grad_()
+    one = {m: (t[:, 0] if m in ("q", "k", "v", "dt", "beta") else t) for m, t in d.items()}
+    state = one.pop("h0")
+    with pytest.raises(RuntimeError, match="forward only"):
+        sss.gated_delta_fwd(**d)
+    with pytest.raises(RuntimeError, match="forward only"):
+        sss.gated_delta_update(state, **one)
+    with torch.no_grad():
+        assert torch.equal(sss.gated_delta_fwd(**d), want)
+        assert torch.isfinite(sss.gated_delta_update(state, **one)).all()
