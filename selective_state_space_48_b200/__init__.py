@@ -936,6 +936,14 @@ def _same(t, dtype, device, shape):
             and t.shape == shape)
 
 
+def _packed_sequences(cu_seqlens, device):
+    """Their number, from the offsets."""
+    _check_views(device, [("cu_seqlens", cu_seqlens, torch.int32, None, "dense")])
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+    return cu_seqlens.shape[0] - 1
+
+
 def _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y,
                   last_state, cu_seqlens, plan, spin_timeout_ns, workspace):
     """The values of ``mss_delta_args`` in order, after the checks."""
@@ -948,12 +956,9 @@ def _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scal
     ind, dev, f32, cu = q.dtype, q.device, torch.float32, 0
     keys, heads, seqs = (batch, L, G, N), (batch, L, H), batch
     if cu_seqlens is not None:
-        _check_views(dev, [("cu_seqlens", cu_seqlens, torch.int32, None, "dense")])
-        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
-            raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+        seqs, cu = _packed_sequences(cu_seqlens, dev), cu_seqlens.data_ptr()
         if batch != 1:
             raise ValueError("packed sequences need batch 1")
-        seqs, cu = cu_seqlens.shape[0] - 1, cu_seqlens.data_ptr()
     states = (seqs, H, P, N)
     if not (_tensors(k, dt, beta, A) and q.is_cuda
             and ind is k.dtype is v.dtype is dt.dtype is beta.dtype
@@ -1055,7 +1060,7 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
     if y is None:
         y = _new(v, out_dtype)
     if return_last_state and last_state is None:
-        seqs = v.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+        seqs = v.shape[0] if cu_seqlens is None else _packed_sequences(cu_seqlens, q.device)
         last_state = torch.empty((seqs, v.shape[2], v.shape[3], q.shape[-1]),
                                  dtype=torch.float32, device=v.device)
     values = _delta_values(q, k, v, dt, A, beta, dt_bias, dt_softplus, beta_sigmoid, scale, h0, y,

@@ -216,3 +216,13 @@ def test_delta_workspace_size_without_a_cut(lib):
     assert size(delta_args(dstate=300)) == UNS
     assert size(delta_args(seqlen=0)) == INV
     assert lib.mss_gated_delta_workspace_size(None, ctypes.byref(n)) == INV
+
+
+@pytest.mark.parametrize("cu", [[0, 40], 3, torch.tensor([0, 40]), torch.zeros(0, dtype=torch.int32),
+                                torch.zeros(1, dtype=torch.int32)])
+def test_offsets_that_are_none_are_refused_by_name(cu):
+    d = dict(q=torch.zeros(1, 40, 1, 8), k=torch.zeros(1, 40, 1, 8), v=torch.zeros(1, 40, 1, 8),
+             dt=torch.zeros(1, 40, 1), A=torch.zeros(1), beta=torch.zeros(1, 40, 1))
+    for last in (False, True):
+        with pytest.raises((TypeError, ValueError), match="cu_seqlens"):
+            sss.gated_delta_fwd(**d, cu_seqlens=cu, return_last_state=last)
