@@ -30,7 +30,11 @@
  *              and then Y = diag(e^c) Q H0^T + (Q K^T o e^(c_t - c_s)) U and
  *              S = e^(c_last) H0 + U^T diag(e^(c_last - c)) K.  Operands that
  *              are not bf16 already enter the products as the sum of two
- *              bf16 values, so the result keeps about 16 bits.  With a
+ *              bf16 values, off by 2^-18 of an operand at most, or of three
+ *              where that would show: last_state and an fp32 y are off by
+ *              about 1e-6 of their size (states that decay slowly, and keys
+ *              that lie close together, several times that, in the recurrent
+ *              evaluation too).  With a
  *              workspace, long sequences of few heads are cut into segments
  *              that run beside each other: the state passes a segment as
  *              S_end = S_start M + B, with M and B from a first pass.

@@ -26,7 +26,16 @@
 // Q K^T o D are fp32 values given as hi + lo, two bf16 values (off by 2^-18
 // at most): a product with an exact operand takes two products, one of two
 // such pairs three (lo lo is left out).  H itself stays in fp32 registers and
-// is added to there, not in the tensor cores' accumulators.
+// is added to there, not in the tensor cores' accumulators.  Two of the pairs
+// made nearly all of the final state's error, 3.6e-6 of its size (U' 2.6e-6, T
+// 2.1e-6, H and R 2e-8 each): U' = U diag(2^(c_last - c)) therefore has a third
+// piece, and so has the diagonal of T, which is b.  That leaves 6.0e-7 (5.4e-7
+// with third pieces of T's 16 x 16 diagonal blocks, for 2 to 3 % of the time)
+// and takes 1 to 2.5 %.  The pairs of the output (U, Q K^T o D) leave y 5e-6
+// off, nothing beside a bf16 y's 2^-9; an fp32 y has third pieces of U and of
+// the 16 x 16 diagonal blocks of Q K^T o D as well, and the product lo lo:
+// 1.3e-6, for 3.5 %.  States that grow old bring H's and R's pairs to the fore:
+// 2.6e-6 for decays about 0.999, where the step form is 1.3e-6 off.
 // The sums c are pairs of fp32 values: a decay is the power of the difference
 // of two of them, and one word alone, rounded to 2^-24 of its size, takes that
 // from every decay behind a hard one (after a step of log2 a = -2300 outputs
@@ -98,7 +107,7 @@ constexpr uint32_t kColH = 0;     // H pairs / the update U'^T K (128)
 constexpr uint32_t kColX = 128;   // H K^T, then the pairs of R, then those of
                                   // U' = U diag(2^(c_last - c))
 constexpr uint32_t kColU = 192;   // U, then its pairs
-constexpr uint32_t kColO1 = 256;  // two
+constexpr uint32_t kColO1 = 256;  // two; third pieces of U', U in the one not in use
 constexpr uint32_t kColO2 = 384;
 constexpr uint32_t kColS = 448;   // K K^T (lanes 0..63), Q K^T (64..127)
 constexpr uint32_t kTmemCols = 512;
@@ -205,13 +214,30 @@ __device__ __forceinline__ float two_sum(float a, float b, float &s) {
 
 __device__ unsigned g_delta_status;
 
+// what a pair of bf16 values leaves of two fp32 ones (exact)
+__device__ __forceinline__ float2 left2(float a, float b, uint32_t p) {
+  float2 r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n fma.rn.f32.bf16 %0, l, %5, %3;\n"
+      " fma.rn.f32.bf16 %1, h, %5, %4;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(p), "f"(a), "f"(b), "h"(static_cast<unsigned short>(0xbf80)));
+  return r;
+}
 // x = hi + lo for a pair of values, packed two to a register
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
   hi = pack_bf16(a, b);
-  const float2 r = __ffma2_rn(
-      make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u)),
-      make_float2(-1.f, -1.f), make_float2(a, b));
+  const float2 r = left2(a, b, hi);
   lo = pack_bf16(r.x, r.y);
+}
+// ... and what that leaves, as a third
+__device__ __forceinline__ uint32_t third2(float a, float b, uint32_t hi, uint32_t lo) {
+  float2 r = left2(a, b, hi);
+  r = left2(r.x, r.y, lo);
+  return pack_bf16(r.x, r.y);
+}
+__device__ __forceinline__ uint4 third8(const float *f, uint4 hi, uint4 lo) {
+  return make_uint4(third2(f[0], f[1], hi.x, lo.x), third2(f[2], f[3], hi.y, lo.y),
+                    third2(f[4], f[5], hi.z, lo.z), third2(f[6], f[7], hi.w, lo.w));
 }
 __device__ __forceinline__ void split8(const float *f, uint4 &hi, uint4 &lo) {
   split2(f[0], f[1], hi.x, lo.x);
@@ -240,6 +266,13 @@ __device__ __forceinline__ void tmem_get16x2(uint32_t a, uint32_t b, float (&v)[
         "=f"(w[0]), "=f"(w[1]), "=f"(w[2]), "=f"(w[3]), "=f"(w[4]), "=f"(w[5]), "=f"(w[6]), "=f"(w[7]), "=f"(w[8]), "=f"(w[9]), "=f"(w[10]), "=f"(w[11]), "=f"(w[12]), "=f"(w[13]), "=f"(w[14]), "=f"(w[15])
       : "r"(a), "r"(b)
       : "memory");
+}
+
+// 4 columns of this thread's lane
+__device__ __forceinline__ void tmem_st4(uint32_t a, const uint32_t (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
 }
 
 // one arrival for the warp, after all its lanes' writes
@@ -381,6 +414,17 @@ __device__ __forceinline__ void invert32(float *a, int lane) {
 constexpr uint32_t kIdKK = idesc_bf16(128, 64, 0, 0);  // both operands K-major
 constexpr uint32_t kIdTK = idesc_bf16(128, 64, 1, 0);  // the first as stored by step
 constexpr uint32_t kLoTile = kHalf >> 4;               // hi -> lo of T and P
+// T and P are lower triangular: slice k (s = 16 k ..) meets the rows and output
+// columns t from 16 k on, so that far into the tile and N that much smaller.
+constexpr uint32_t kTriN = 2u << 17;
+__device__ __forceinline__ constexpr uint32_t tri(int k) { return static_cast<uint32_t>(k * 130); }
+// Third pieces of their 16 x 16 diagonal blocks lie in the hi tile above the
+// diagonal: block k in rows 16 (k / 2) .., columns 32 + 16 (k % 2) ..
+// (of T's only the diagonal is not 0)
+constexpr uint32_t kId16KK = idesc_bf16(128, 16, 0, 0), kId16TK = idesc_bf16(128, 16, 1, 0);
+__device__ __forceinline__ constexpr uint32_t diag3(int k) {
+  return static_cast<uint32_t>((k >> 1) * 128 + 4 + 2 * (k & 1));
+}
 // slice k of a K-major tile whose 64-wide halves lie 2 kHalf apart
 __device__ __forceinline__ constexpr uint32_t kslice(int k) {
   return static_cast<uint32_t>((k >> 2) * (2 * kHalf >> 4) + (k & 3) * 2);
@@ -395,6 +439,8 @@ template <typename OutT, int NK, bool VEC>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chunk_kernel(const __grid_constant__ Maps maps, const DeltaParams p, const int y_tma) {
   constexpr uint32_t idH = idesc_bf16(128, 16 * NK, 0, 1);  // the second as stored by step
+  // an fp32 output: its products with third pieces too
+  constexpr bool kWide = sizeof(OutT) == 4;
   // the swizzle needs 1024-byte tiles; a block without static shared memory
   // has its dynamic memory on such a boundary
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -601,8 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dV = desc_lo(sbase + oV, kHalf);
 #pragma unroll 2
         for (int k = 0; k < 4; ++k) {
-          mma_ss(kColU, dV + k * 128, dT + k * 2, kIdTK, k > 0, on);
-          mma_ss(kColU, dV + k * 128, dT + kLoTile + k * 2, kIdTK, 1, on);
+          const uint32_t d = kColU + 16 * k, id = kIdTK - k * kTriN;
+          mma_ss(d, dV + k * 128, dT + tri(k), id, k > 0, on);
+          mma_ss(d, dV + k * 128, dT + kLoTile + tri(k), id, 1, on);
+          mma_ss(d, dV + k * 128, dT + diag3(k), kId16TK, 1, on);
         }
       }
       mma_commit(bar + kEmptyV, on);
@@ -611,9 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       {  // U^T += R^T T^T
 #pragma unroll 2
         for (int k = 0; k < 4; ++k) {
-          mma_ts(kColU, kColX + 16 * k, dT + k * 2, kIdKK, 1, on);
-          mma_ts(kColU, kColX + 16 * k + 8, dT + k * 2, kIdKK, 1, on);
-          mma_ts(kColU, kColX + 16 * k, dT + kLoTile + k * 2, kIdKK, 1, on);
+          const uint32_t d = kColU + 16 * k, id = kIdKK - k * kTriN;
+          mma_ts(d, kColX + 16 * k, dT + tri(k), id, 1, on);
+          mma_ts(d, kColX + 16 * k + 8, dT + tri(k), id, 1, on);
+          mma_ts(d, kColX + 16 * k, dT + kLoTile + tri(k), id, 1, on);
         }
       }
       mma_commit(bar + kDoneU, on);
@@ -631,6 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sy.wait(kDoneO1, i & 1);  // the update overwrites the pairs of H
       sy.wait(kReadyU, i & 1);
       tc_fence_after();
+      const uint32_t col3 = kColO1 + (~i & 1) * 64;  // third pieces of U', U
       {  // U'^T K
         const uint32_t dK = desc_lo(kq, 2 * kHalf);
 #pragma unroll 2
@@ -638,6 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts(kColH, kColX + 16 * k, dK + k * 128, idH, k > 0, on);
           mma_ts(kColH, kColX + 16 * k + 8, dK + k * 128, idH, 1, on);
         }
+#pragma unroll 2
+        for (int k = 0; k < 4; ++k) mma_ts(kColH, col3 + 16 * k, dK + k * 128, idH, 1, on);
       }
       mma_commit(bar + kDoneH, on);
       if (!y_tma) mma_commit(bar + kEmptyKQ + st, on);
@@ -648,9 +700,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t dP = desc_lo(sbase + oP + (i & 1) * 2 * kHalf, 16);
 #pragma unroll 2
         for (int k = 0; k < 4; ++k) {
-          mma_ts(kColO2, kColU + 16 * k, dP + k * 2, kIdKK, k > 0, on);
-          mma_ts(kColO2, kColU + 16 * k + 8, dP + k * 2, kIdKK, 1, on);
-          mma_ts(kColO2, kColU + 16 * k, dP + kLoTile + k * 2, kIdKK, 1, on);
+          const uint32_t d = kColO2 + 16 * k, u = kColU + 16 * k, id = kIdKK - k * kTriN;
+          mma_ts(d, u, dP + tri(k), id, k > 0, on);
+          mma_ts(d, u + 8, dP + tri(k), id, 1, on);
+          mma_ts(d, u, dP + kLoTile + tri(k), id, 1, on);
+          if constexpr (kWide) {
+            mma_ts(d, u + 8, dP + kLoTile + tri(k), id, 1, on);
+            mma_ts(d, col3 + 16 * k + 8, dP + tri(k), id, 1, on);
+            mma_ts(d, u, dP + diag3(k), kId16KK, 1, on);
+          }
         }
       }
       mma_commit(bar + kDoneO, on);
@@ -879,25 +937,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       gam = du[2 * C - 1];
       tc_fence_after();
       {
+        // (third pieces go into the columns of the O1 before, which this warp has
+        // read and O1 of the next chunk takes after O2 of this one; 8 steps at
+        // a time, for the registers)
+        const uint32_t col3 = tl + kColO1 + (~i & 1) * 64 + 16 * e;
         float v[16];
-        uint32_t hi[8], lo[8];
         tmem_get16(tl + kColU + 16 * e, v);
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 d = *reinterpret_cast<const float4 *>(du + 16 * e + j);
-          split2(v[j] * d.x, v[j + 1] * d.y, hi[j / 2], lo[j / 2]);
-          split2(v[j + 2] * d.z, v[j + 3] * d.w, hi[j / 2 + 1], lo[j / 2 + 1]);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[4], lo[4], t[4];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const float4 d = *reinterpret_cast<const float4 *>(du + 16 * e + 8 * c + j);
+            const float a0 = v[8 * c + j] * d.x, a1 = v[8 * c + j + 1] * d.y;
+            const float a2 = v[8 * c + j + 2] * d.z, a3 = v[8 * c + j + 3] * d.w;
+            split2(a0, a1, hi[j / 2], lo[j / 2]);
+            split2(a2, a3, hi[j / 2 + 1], lo[j / 2 + 1]);
+            t[j / 2] = third2(a0, a1, hi[j / 2], lo[j / 2]);
+            t[j / 2 + 1] = third2(a2, a3, hi[j / 2 + 1], lo[j / 2 + 1]);
+          }
+          tmem_st4(tl + kColX + 16 * e + 4 * c, hi);
+          tmem_st4(tl + kColX + 16 * e + 8 + 4 * c, lo);
+          tmem_st4(col3 + 4 * c, t);
         }
-        tmem_st8(tl + kColX + 16 * e, hi);
-        tmem_st8(tl + kColX + 16 * e + 8, lo);
         tmem_wait_st();
         tc_fence_before();
         warp_arrive(bar + kReadyU, lane);
-        // (the pairs that only the output needs)
+        // (the pieces that only the output needs)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) split2(v[2 * j], v[2 * j + 1], hi[j], lo[j]);
-        tmem_st8(tl + kColU + 16 * e, hi);
-        tmem_st8(tl + kColU + 16 * e + 8, lo);
+        for (int c = 0; c < 2; ++c) {
+          uint32_t hi[4], lo[4], t[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float a = v[8 * c + 2 * j], b = v[8 * c + 2 * j + 1];
+            split2(a, b, hi[j], lo[j]);
+            if (kWide) t[j] = third2(a, b, hi[j], lo[j]);
+          }
+          tmem_st4(tl + kColU + 16 * e + 4 * c, hi);
+          tmem_st4(tl + kColU + 16 * e + 8 + 4 * c, lo);
+          if (kWide) tmem_st4(col3 + 8 + 4 * c, t);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -924,10 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float *beta_s = reinterpret_cast<const float *>(sm + oGate + gr * kGate);
     const float *neg_s = beta_s + C;  // -c: the high words, then the low ones
 
-    // the blocks of P and T above the diagonal stay zero
-    for (int k = at; k < 4 * 32 * 4; k += kAux)
-      *reinterpret_cast<uint4 *>((k < 256 ? pt : tt) + ((k >> 7) & 1) * kHalf +
-                                 swz((k >> 2) & 31, 4 + (k & 3))) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4 *>(tt + swz(at >> 2, 4 + (at & 3))) = make_uint4(0u, 0u, 0u, 0u);
 
     for (int i = gr; i < nc; i += 2) {
       const int st = i % 3;
@@ -1001,6 +1077,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t o = swz(t, 4 * e + 2 * c + k);
             *reinterpret_cast<uint4 *>(pt + o) = hi;
             *reinterpret_cast<uint4 *>(pt + kHalf + o) = lo;
+            if (kWide && diag && c == lane >> 4)
+              *reinterpret_cast<uint4 *>(pt + swz(16 * blk + (lane & 15), 4 + 2 * c + k)) =
+                  third8(f + 8 * k, hi, lo);
           }
         }
         // A22 is there for the warp of q = 2
@@ -1038,6 +1117,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t o = swz(32 * w + r, 4 * w + c);
         *reinterpret_cast<uint4 *>(tt + o) = hi;
         *reinterpret_cast<uint4 *>(tt + kHalf + o) = lo;
+      }
+      if (at < C) {  // the third piece of T's diagonal
+        const float b = beta_s[at];
+        const uint32_t hi = pack_bf16(b, 0.f), lo = pack_bf16(b - __uint_as_float(hi << 16), 0.f);
+        *reinterpret_cast<__nv_bfloat16 *>(
+            tt + swz(16 * (at >> 5) + (at & 15), 4 + ((at >> 3) & 3)) + 2 * (at & 7)) =
+            __float2bfloat16_rn((b - __uint_as_float(hi << 16)) - __uint_as_float(lo << 16));
       }
       bar_sync(kBarAux + gr, kAux);
       prod_n<32>(scr + bA22 * kBlk + r2 * kLd, scr + bZ * kBlk + c4, z);

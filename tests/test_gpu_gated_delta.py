@@ -785,3 +785,27 @@ def test_inputs_that_require_gradients_are_refused(n):
     with torch.no_grad():
         assert torch.equal(sss.gated_delta_fwd(**d), want)
         assert torch.isfinite(sss.gated_delta_update(state, **one)).all()
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("plan", ["recurrent", "chunked"])
+def test_one_chunk_of_unit_keys_keeps_fp32(plan, out_dtype):
+    """64 different unit vectors as keys, the queries the same ones, no decay:
+    column t of the state is b_t v_t and y_t = scale b_t v_t, one term each, so
+    every value can be held to fp32 by itself.  In half steps (2^-24) of the
+    value: b about 10 (the argument's and the sum's rounding, an exponential
+    good to 3, a quotient good to 4), b v 1, and two products' sums of three
+    pieces, each a truncation (2) of a whole: 24; y: six more, and two for the
+    scale: 38.  (b v in two bf16 pieces would be up to 64 off, b as well.)"""
+    P = 128
+    d = delta_inputs(1, 64, 2, P, 1, 64, BF, seed=11)
+    d["q"] = d["k"] = torch.eye(64, device="cuda", dtype=BF).view(1, 64, 1, 64)
+    d["A"] = torch.zeros(2, device="cuda")
+    y, last = sss.gated_delta_fwd(**d, scale=0.1, return_last_state=True, out_dtype=out_dtype,
+                                  plan=PLANS[plan], check_status=True)
+    u = torch.sigmoid(d["beta"].double())[..., None] * d["v"].double()  # (1, 64, 2, P)
+    want = u[0].permute(1, 2, 0)  # heads, rows, columns
+    assert ((last[0] - want).abs() <= 24 * 2.0 ** -24 * want.abs()).all()
+    half = 38 * 2.0 ** -24 + (2.0 ** -8 if out_dtype == BF else 0)
+    scaled = float(torch.tensor(0.1)) * u
+    assert ((y.double() - scaled).abs() <= half * scaled.abs()).all()
