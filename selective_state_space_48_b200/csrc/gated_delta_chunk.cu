@@ -188,6 +188,7 @@ struct Waits {
   // short limit
   __device__ __forceinline__ void drain(int i, uint32_t parity) const {
     uint32_t n = 0;
+#pragma unroll 1
     while (!try_wait(i, parity))
       if (++n >= kDrainTries) {
         *abort = 1;
