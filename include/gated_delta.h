@@ -61,7 +61,7 @@
  * its own h0 and last_state; an empty one hands h0 (or 0) to last_state.
  * Rows of y outside every sequence are not written.
  * Limits: dstate <= 256, any headdim.  Pointers are aligned to their element
- * size.  The chunked evaluation takes bf16 inputs with dstate a multiple of 8
+ * size.  Sizes of 0 are errors.  The chunked evaluation takes bf16 inputs with dstate a multiple of 8
  * up to 128, headdim a multiple of 8, q, k, v 16-byte aligned and their
  * strides multiples of 8; everything else runs the recurrent one, or,
  * with a workspace and dstate <= 128, is copied first.
@@ -87,7 +87,10 @@ extern "C" {
 #endif
 
 /* mss_delta_args.plan: which evaluation runs */
-#define MSS_DELTA_AUTO 0      /* chosen by type, sizes, alignment and length */
+/* AUTO: chosen by type, sizes, alignment and length; of packed sequences by
+ * their average length, seqlen / num_seqs, so a pack of a long one and many
+ * short ones may be better off with CHUNKED */
+#define MSS_DELTA_AUTO 0
 #define MSS_DELTA_RECURRENT 1
 #define MSS_DELTA_CHUNKED 2   /* MSS_ERR_UNSUPPORTED where it does not apply */
 

@@ -34,7 +34,7 @@
  * element size; rows of 16-byte vectors run faster.
  * residual_out may be the residual's own memory (same stride), dresidual
  * may be dresidual_out's, dx or dz may be dy's; other outputs must not
- * overlap inputs.
+ * overlap inputs.  Sizes of 0 are errors.
  *
  * Ownership, streams and errors as in selective_scan.h.
  */

@@ -1044,7 +1044,12 @@ def gated_delta_fwd(q, k, v, dt, A, beta, dt_bias=None, dt_softplus=True, beta_s
     num_seqs + 1 ascending offsets within 0 ... L) packs independent
     sequences into one row (batch 1); rows of y outside them are not
     written.  h0 and last_state: (sequences, nheads, headdim, dstate)
-    float32, and may be one tensor.  Returns y (batch, L, nheads, headdim) in
+    float32, and may be one tensor; y must not overlap the inputs.  ``plan``:
+    MSS_DELTA_AUTO goes by the length (of packed sequences by the average),
+    MSS_DELTA_CHUNKED suits a pack of a long sequence and many short ones too,
+    MSS_DELTA_RECURRENT keeps fp32 throughout.  With ``stream`` the call runs,
+    and allocates, on that stream; the inputs have to be ready there.  Returns
+    y (batch, L, nheads, headdim) in
     ``out_dtype`` (and the final states when ``return_last_state``).  Forward
     only: an input that requires a gradient is refused outside of
     ``torch.no_grad()``.

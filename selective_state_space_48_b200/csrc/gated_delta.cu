@@ -13,8 +13,8 @@
 //
 // One token (the decode step) is bound by reading and writing the fp32 state
 // (8 headdim dstate bytes per head), every load of which is issued before the
-// arithmetic: 192 sequences of 32 heads of 128 x 128 take 127 us, 97 % of the
-// copy bandwidth.
+// arithmetic: 192 sequences of 32 heads of 128 x 128 take 124 to 127 us, 97 to
+// 99 % of the copy bandwidth.
 //
 // Over more steps the chain of a step (dots, three shuffles, update) bounds it.
 // What does not hang on the state is kept out of that chain: a tile of TB steps
@@ -36,15 +36,17 @@ namespace sss48 {
 namespace {
 
 constexpr int kThreads = 128;
-// Steps of a sequence (packed ones: on average) from which the chunked
-// evaluation runs.  Steps against chunks, us, 32 heads of 128 x 128 in bf16:
-// of one sequence 8.0 / 16.7 at 16 steps, 13.5 / 16.3 at 32, 24 / 16 at 64; of
-// 8 sequences 24 / 33, 42 / 32, 79 / 33; of 32 86 / 119, 156 / 118, 300 / 127.
+// Steps of a sequence (packed ones: on average, their lengths are on the device;
+// a pack of one long sequence and many short ones is therefore worth an explicit
+// plan: 8000 steps beside 300 single ones 3719 us, 1570 in chunks) from which the
+// chunked evaluation runs.  Steps against chunks, us, 32 heads of 128 x 128 in
+// bf16: of one sequence 10.4 / 15.4 at 16 steps, 14.6 / 14.8 at 32, 27 / 15 at
+// 64; of 8 sequences 25 / 30, 44 / 29, 82 / 29; of 32 84 / 97, 156 / 95, 304 / 95.
 constexpr int64_t kChunkSteps = 32;
 // ... and where q, k, v are copied for it first (sizes, strides or addresses
 // that tensor maps do not take): one sequence of 32 heads of 100 x 100, steps
-// against copy and chunks, us: 20 / 16 at 48 steps, 27 / 17 at 64, 48 / 22 at
-// 128; 8 of 2048 2607 / 519.
+// against copy and chunks, us: 21 / 20 at 48 steps, 27 / 21 at 64, 50 / 25 at
+// 128; 8 of 2048 2608 / 525.
 constexpr int64_t kCopySteps = 48;
 
 // Four columns from `col` of a row of n columns: one vector load where VEC,

@@ -137,9 +137,9 @@ __device__ __forceinline__ int bar_count(int i) {
 
 // Bounded waits, short since every one is inlined: instructions from beyond
 // the instruction caches bound this kernel where every SM runs it (108 KB of
-// code took twice the time; 78 KB, with the products unrolled, 292 us for 8 x
-// 2048 steps, 71 KB, with them in loops, 275, though alone on its SMs the
-// longer form is 2 % faster).  A try suspends the thread for up to 4.0 us
+// code took twice the time; 8 x 2048 steps with the products unrolled 292 us,
+// with them in loops, 7 KB less, 275, though alone on its SMs the longer form is
+// 2 % faster).  It is 81 KB.  A try suspends the thread for up to 4.0 us
 // (measured: hints of 1 ns to 1 ms gave the same), and a wait gives up after
 // `limit` of them (read off the clock instead, the limit made the kernel 2 to 3
 // % slower by its size).  Then, and once any wait of the block has given up,
@@ -1354,7 +1354,7 @@ cudaError_t launch_delta_copy(DeltaParams *p, void *to, cudaStream_t stream) {
 // work on two chains of 1 / segs the length.
 // Times in chunks, a block's start taken as 3 of them and the join as 2.5 and
 // one more for every further segment.  8192 steps of 32 heads of 128 x 128 take
-// 361 us, 470 whole; of 8 heads 156, 450 whole; 2048 of 32 heads 109 and 123.
+// 389 us, 492 whole; of 8 heads 168, 478 whole; 2048 of 32 heads 117 and 130.
 int delta_segments(const DeltaParams &p, int sms, int *seg_chunks, int64_t *floats) {
   const int64_t heads = p.seqs * p.H, tasks = heads * ((p.P + 127) / 128), nc = (p.L + C - 1) / C;
   const auto waves = [&](int64_t blocks) { return (blocks + sms - 1) / sms; };
