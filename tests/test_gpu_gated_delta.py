@@ -809,3 +809,29 @@ def test_one_chunk_of_unit_keys_keeps_fp32(plan, out_dtype):
     half = 38 * 2.0 ** -24 + (2.0 ** -8 if out_dtype == BF else 0)
     scaled = float(torch.tensor(0.1)) * u
     assert ((y.double() - scaled).abs() <= half * scaled.abs()).all()
+
+
+def test_a_forked_stream_in_a_captured_graph():
+    """A graph whose captured stream forks into another, on which the calls
+    run (with a workspace, and with gradients' partial sums), replayed: the
+    bits of calls alone."""
+    d = delta_inputs(1, 1500, 2, 64, 1, 64, BF, h0=True)
+    x, z = torch.randn(2, 64, 512, device="cuda")
+    w = torch.ones(512, device="cuda")
+    want = sss.gated_delta_fwd(**d, return_last_state=True)
+    grads = sss.gated_rmsnorm_bwd(x, z, w, z)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = sss.gated_delta_fwd(**d, return_last_state=True, stream=side)
+        g = sss.gated_rmsnorm_bwd(x, z, w, z, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for _ in range(2):
+        for t in (*got, *g.values()):
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert all(torch.equal(g[n], grads[n]) for n in grads)
+    assert sss.gated_delta_status() == sss.MSS_OK
